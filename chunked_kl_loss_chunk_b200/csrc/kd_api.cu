@@ -177,9 +177,13 @@ static kd_status fwd_entry(const void* h, const void* W, int dtype, int64_t T, i
     return KD_ERR_INVALID_ARG;
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
-  return kd::fused_fwd(h, W, dtype, T, T_norm, d, V, t_vals, t_idx, K, chunk, temperature, flags,
-                       loss, lse, kl_rows, ws, static_cast<cudaStream_t>(stream), sms,
-                       kd::wait_limit_ns());
+  kd::RowTerms rt;
+  rt.t_vals = t_vals;
+  rt.t_idx = t_idx;
+  rt.K = K;
+  rt.flags = flags;
+  return kd::fused_fwd(h, W, dtype, T, T_norm, d, V, rt, chunk, temperature, loss, lse, kl_rows, ws,
+                       static_cast<cudaStream_t>(stream), sms, kd::wait_limit_ns());
 }
 
 static kd_status bwd_entry(const void* h, const void* W, int dtype, int64_t T, int64_t T_norm,
@@ -199,9 +203,14 @@ static kd_status bwd_entry(const void* h, const void* W, int dtype, int64_t T, i
     return KD_ERR_INVALID_ARG;
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
-  return kd::fused_bwd(h, W, dtype, T, T_norm, d, V, t_vals, t_idx, K, chunk, temperature, flags,
-                       lse, grad_loss, dH, dW, accumulate_dW, ws,
-                       static_cast<cudaStream_t>(stream), sms, kd::wait_limit_ns());
+  kd::RowTerms rt;
+  rt.t_vals = t_vals;
+  rt.t_idx = t_idx;
+  rt.K = K;
+  rt.flags = flags;
+  return kd::fused_bwd(h, W, dtype, T, T_norm, d, V, rt, chunk, temperature, lse, grad_loss, dH, dW,
+                       accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
+                       kd::wait_limit_ns());
 }
 
 extern "C" {
@@ -257,6 +266,65 @@ kd_status kd_fused_kl_bwd_shard(const void* h, const void* W, int dtype, int64_t
                                 int accumulate_dW, void* ws, size_t ws_bytes, void* stream) {
   return bwd_entry(h, W, dtype, T, T_total, d, V, t_vals, t_idx, K, chunk, temperature, flags, lse,
                    grad_loss, dH, dW, accumulate_dW, ws, ws_bytes, stream);
+}
+
+size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int dtype,
+                                      int backward) {
+  if (T < 1 || d < 1 || V < 1 || chunk < 1) return 0;
+  const kd::WsLayout L = kd::ws_layout(T, d, V, 1, chunk, dtype);
+  return L.ok ? (backward ? L.total : L.fwd_end) : 0;
+}
+
+// Checks shared by the two calls below; `need` is WsLayout::fwd_end or ::total.
+static kd_status validate_head(const void* h, const void* W, int dtype, int64_t T, int64_t d,
+                               int64_t V, const int32_t* targets, int64_t chunk, float tau,
+                               void* ws, size_t ws_bytes, size_t kd::WsLayout::*need) {
+  // one entry per row: `targets` stands in for both arrays of a cache with K = 1
+  const kd_status st =
+      kd::validate_loss_inputs(h, W, dtype, T, d, V, reinterpret_cast<const float*>(targets),
+                               targets, 1, chunk, tau);
+  if (st != KD_OK) return st;
+  if (!ws || !aligned(ws, kd::KD_WS_ALIGN)) return KD_ERR_INVALID_ARG;
+  const kd::WsLayout L = kd::ws_layout(T, d, V, 1, chunk, dtype);
+  if (!L.ok || ws_bytes < L.*need) return KD_ERR_WORKSPACE;
+  return KD_OK;
+}
+
+kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
+                              int64_t V, const int32_t* targets, int64_t chunk, float temperature,
+                              float* logp, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  const kd_status st = validate_head(h, W, dtype, T, d, V, targets, chunk, temperature, ws,
+                                     ws_bytes, &kd::WsLayout::fwd_end);
+  if (st != KD_OK) return st;
+  if (!logp || !lse || !aligned(logp, 16) || !aligned(lse, 16)) return KD_ERR_INVALID_ARG;
+  const int sms = num_sms_current();
+  if (sms <= 0) return KD_ERR_CUDA;
+  kd::RowTerms rt;
+  rt.targets = targets;
+  return kd::fused_fwd(h, W, dtype, T, 1, d, V, rt, chunk, temperature, nullptr, lse, logp, ws,
+                       static_cast<cudaStream_t>(stream), sms, kd::wait_limit_ns());
+}
+
+kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
+                              int64_t V, const int32_t* targets, int64_t chunk, float temperature,
+                              const float* lse, const float* grad_logp, const float* grad_loss,
+                              void* dH, float* dW, int accumulate_dW, void* ws, size_t ws_bytes,
+                              void* stream) {
+  const kd_status st = validate_head(h, W, dtype, T, d, V, targets, chunk, temperature, ws,
+                                     ws_bytes, &kd::WsLayout::total);
+  if (st != KD_OK) return st;
+  if (!lse || !grad_logp || (!dH && !dW)) return KD_ERR_INVALID_ARG;
+  if (!aligned(lse, 16) || !aligned(grad_logp, 16) || !aligned(dH, 16) || !aligned(dW, 16) ||
+      (grad_loss && !aligned(grad_loss, 4)))
+    return KD_ERR_INVALID_ARG;
+  const int sms = num_sms_current();
+  if (sms <= 0) return KD_ERR_CUDA;
+  kd::RowTerms rt;
+  rt.targets = targets;
+  rt.grad_rows = grad_logp;
+  return kd::fused_bwd(h, W, dtype, T, 1, d, V, rt, chunk, temperature, lse, grad_loss, dH, dW,
+                       accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
+                       kd::wait_limit_ns());
 }
 
 kd_status kd_read_device_status(const void* ws, void* stream) {

@@ -50,20 +50,32 @@ kd_status validate_loss_inputs(const void* h, const void* W, int dtype, int64_t 
                                int64_t V, const float* t_vals, const int32_t* t_idx, int K,
                                int64_t chunk, float tau);
 
+// What a row of the head's logits is reduced to: the KL against K cached
+// teacher entries, or (targets non-null, K == 1) the log-probability of one
+// target, whose backward takes the gradient of each row's log-probability.
+struct RowTerms {
+  const float* t_vals = nullptr;
+  const int32_t* t_idx = nullptr;
+  int K = 1;
+  uint32_t flags = 0;
+  const int32_t* targets = nullptr;
+  const float* grad_rows = nullptr;
+};
+
 // The fused loss over T positions whose loss and gradients are normalised by
 // T_norm >= T: T_norm == T for a whole batch, the batch's total positions when
 // these T rows are one data-parallel shard of it (then the shards' losses and
-// dW contributions sum to the batch's).
+// dW contributions sum to the batch's).  Log-probabilities of targets pass
+// T_norm == 1, and loss == null (no mean is taken).  row_out: KL_t or logp_t.
 kd_status fused_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t T_norm, int64_t d,
-                    int64_t V, const float* t_vals, const int32_t* t_idx, int K, int64_t chunk,
-                    float tau, uint32_t flags, float* loss, float* lse, float* kl_rows, void* ws,
-                    cudaStream_t s, int num_sms, uint64_t limit_ns);
+                    int64_t V, const RowTerms& rt, int64_t chunk, float tau, float* loss,
+                    float* lse, float* row_out, void* ws, cudaStream_t s, int num_sms,
+                    uint64_t limit_ns);
 
 kd_status fused_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t T_norm, int64_t d,
-                    int64_t V, const float* t_vals, const int32_t* t_idx, int K, int64_t chunk,
-                    float tau, uint32_t flags, const float* lse, const float* grad_loss, void* dH,
-                    float* dW, int accumulate, void* ws, cudaStream_t s, int num_sms,
-                    uint64_t limit_ns);
+                    int64_t V, const RowTerms& rt, int64_t chunk, float tau, const float* lse,
+                    const float* grad_loss, void* dH, float* dW, int accumulate, void* ws,
+                    cudaStream_t s, int num_sms, uint64_t limit_ns);
 
 // The top-K build's workspace: the status word at byte 0 and the row counter
 // (zero before each build) at byte 8.

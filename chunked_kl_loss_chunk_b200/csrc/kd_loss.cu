@@ -252,10 +252,36 @@ prep_reg_kernel(const float* __restrict__ vals, const int32_t* __restrict__ idx,
   }
 }
 
+// Row preparation for log-probabilities of one target per row: the GEMM
+// epilogues see a cache of one entry.  Forward (grad == null): p = S = 1, so
+// the gather is z_y.  Backward: p = S = -g_t, so that the dz epilogue's
+//   coef (S softmax - p [v == y])  is  g_t / tau ([v == y] - softmax),
+// the gradient of g_t logp_t.  A row whose target is KD_TARGET_IGNORE gets
+// p = S = 0 and an index past V (its g_t is not read); any other target outside
+// [0, V) gets the same and records KD_ERR_BAD_INDEX.
+__global__ void __launch_bounds__(256)
+prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict__ grad, int64_t T,
+                   int64_t V, int32_t* __restrict__ idx_sorted, float* __restrict__ p_sorted,
+                   float2* __restrict__ stats, uint32_t* status) {
+  griddep_launch_dependents();
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < T;
+       t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int32_t y = targets[t];
+    const bool ok = y >= 0 && static_cast<int64_t>(y) < V;
+    const float p = !ok ? 0.f : (grad ? -grad[t] : 1.f);
+    idx_sorted[t] = ok ? y : INT32_MAX;
+    p_sorted[t] = p;
+    stats[t] = make_float2(p, 0.f);
+    if (!ok && y != KD_TARGET_IGNORE) set_status(status, KD_ERR_BAD_INDEX);
+  }
+}
+
 // ----------------------------------------------------------------------------
 // K4: combine the per-(row, vocab tile) partials of one chunk.  One warp per
 // row; lane l merges tiles l, l+32, ... in order, then a fixed shuffle tree.
 //   LSE_t = M/tau + ln S,  KL_t = sum p log p - G/tau + (sum p) LSE_t
+// or, with LOGP (one target per row, p = 1 at it):
+//   logp_t = G/tau - LSE_t, and 0 for a row without a target (p = 0).
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void merge_lse(float& m, float& s, float m2, float s2, float zs) {
   const float nm = fmaxf(m, m2);
@@ -264,6 +290,7 @@ __device__ __forceinline__ void merge_lse(float& m, float& s, float m2, float s2
   m = nm;
 }
 
+template <bool LOGP>
 __global__ void __launch_bounds__(256)
 combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64_t row0,
                float zscale, float inv_tau, const float2* __restrict__ stats,
@@ -303,7 +330,8 @@ combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64
     const float L = m * inv_tau + logf(s);
     const float2 st = stats[t];
     lse[t] = L;
-    kl[t] = st.y - gsum * inv_tau + st.x * L;
+    if constexpr (LOGP) kl[t] = st.x != 0.f ? gsum * inv_tau - L : 0.f;
+    else kl[t] = st.y - gsum * inv_tau + st.x * L;
   }
 }
 
@@ -448,23 +476,27 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned block, cu
   return cudaGetLastError();
 }
 
-// Cache preparation for fwd_impl / bwd_impl.  K <= 128: the register sort, a
-// grid small enough to be resident at once, so that the first GEMM (launched
-// with programmatic serialization) can start while it runs.  Larger K: the
-// shared-memory sort.
-cudaError_t launch_prep(const float* t_vals, const int32_t* t_idx, int64_t T, int K, int64_t V,
-                        float inv_tau, int logprob, int32_t* idx_s, float* p_s, float2* stats,
-                        uint32_t* status, cudaStream_t s, int num_sms) {
+// Row preparation for fwd_impl / bwd_impl.  One target per row: the target
+// kernel.  A cache with K <= 128: the register sort, a grid small enough to be
+// resident at once, so that the first GEMM (launched with programmatic
+// serialization) can start while it runs.  Larger K: the shared-memory sort.
+cudaError_t launch_prep(const RowTerms& rt, int64_t T, int64_t V, float inv_tau, int32_t* idx_s,
+                        float* p_s, float2* stats, uint32_t* status, cudaStream_t s, int num_sms) {
   const int64_t blocks64 = (T + PREP_WARPS - 1) / PREP_WARPS;
-  if (K <= PREP_REG_MAXK) {
-    const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+  const int logprob = (rt.flags & KD_KL_LOGPROB_CACHE) ? 1 : 0;
+  if (rt.targets) {
+    const int64_t b = (T + 255) / 256;
+    prep_target_kernel<<<static_cast<unsigned>(b < cap ? b : cap), 256, 0, s>>>(
+        rt.targets, rt.grad_rows, T, V, idx_s, p_s, stats, status);
+  } else if (rt.K <= PREP_REG_MAXK) {
     const unsigned blocks = static_cast<unsigned>(blocks64 < cap ? blocks64 : cap);
-    prep_reg_kernel<<<blocks, PREP_WARPS * 32, 0, s>>>(t_vals, t_idx, T, K, V, inv_tau, logprob,
-                                                        idx_s, p_s, stats, status);
+    prep_reg_kernel<<<blocks, PREP_WARPS * 32, 0, s>>>(rt.t_vals, rt.t_idx, T, rt.K, V, inv_tau,
+                                                        logprob, idx_s, p_s, stats, status);
   } else {
     const int blocks = static_cast<int>(blocks64 < 65535 * 16 ? blocks64 : 65535 * 16);
     prep_kernel<<<blocks, PREP_WARPS * 32, PREP_WARPS * PREP_MAXK * 8, s>>>(
-        t_vals, t_idx, T, K, V, inv_tau, logprob, idx_s, p_s, stats, status);
+        rt.t_vals, rt.t_idx, T, rt.K, V, inv_tau, logprob, idx_s, p_s, stats, status);
   }
   count_launch();
   return cudaGetLastError();
@@ -623,25 +655,23 @@ WsLayout ws_layout(int64_t T, int64_t d, int64_t V, int K, int64_t chunk, int dt
 
 template <typename Elem>
 static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_norm, int64_t d,
-                          int64_t V, const float* t_vals, const int32_t* t_idx, int K,
-                          int64_t chunk, float tau, uint32_t flags, float* loss, float* lse,
-                          float* kl_rows, void* ws, cudaStream_t s, int num_sms,
+                          int64_t V, const RowTerms& rt, int64_t chunk, float tau, float* loss,
+                          float* lse, float* row_out, void* ws, cudaStream_t s, int num_sms,
                           uint64_t limit_ns) {
   constexpr bool F32 = sizeof(Elem) == 4;
   constexpr int BK = ElemCfg<Elem>::BK;
-  const WsLayout L = ws_layout(T, d, V, K, chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
+  const WsLayout L = ws_layout(T, d, V, rt.K, chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
   unsigned char* w = static_cast<unsigned char*>(ws);
   uint32_t* status = reinterpret_cast<uint32_t*>(w);
   int32_t* idx_s = reinterpret_cast<int32_t*>(w + L.idx_sorted);
   float* p_s = reinterpret_cast<float*>(w + L.p_sorted);
   float2* stats = reinterpret_cast<float2*>(w + L.stats);
-  float* kl = kl_rows ? kl_rows : reinterpret_cast<float*>(w + L.kl);
+  float* row = row_out ? row_out : reinterpret_cast<float*>(w + L.kl);
   float4* part = reinterpret_cast<float4*>(w + L.scratch);
 
   if (cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return KD_ERR_CUDA;
   const float inv_tau = 1.f / tau;
-  if (launch_prep(t_vals, t_idx, T, K, V, inv_tau, (flags & KD_KL_LOGPROB_CACHE) ? 1 : 0, idx_s,
-                  p_s, stats, status, s, num_sms) != cudaSuccess)
+  if (launch_prep(rt, T, V, inv_tau, idx_s, p_s, stats, status, s, num_sms) != cudaSuccess)
     return KD_ERR_CUDA;
   CUtensorMap tW;
   if (!make_map(&tW, W, F32, d, V, d, BK, 128)) return KD_ERR_CUDA;
@@ -663,7 +693,7 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
     g.k_split = 1;
     g.row0 = c0;
     g.V = V;
-    g.Ktop = K;
+    g.Ktop = rt.K;
     g.zscale = zscale;
     g.idx_sorted = idx_s;
     g.p_sorted = p_s;
@@ -675,12 +705,14 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
         cudaSuccess)
       return KD_ERR_CUDA;
     const int cblocks = cdiv(rows * 32, 256);
-    if (launch_pdl(combine_kernel, static_cast<unsigned>(cblocks), 256u, s,
-                   static_cast<const float4*>(part), static_cast<int>(rows), g.n_tiles, c0, zscale,
-                   inv_tau, static_cast<const float2*>(stats), lse, kl) != cudaSuccess)
+    if (launch_pdl(rt.targets ? combine_kernel<true> : combine_kernel<false>,
+                   static_cast<unsigned>(cblocks), 256u, s, static_cast<const float4*>(part),
+                   static_cast<int>(rows), g.n_tiles, c0, zscale, inv_tau,
+                   static_cast<const float2*>(stats), lse, row) != cudaSuccess)
       return KD_ERR_CUDA;
   }
-  mean_kernel<<<1, 1024, 0, s>>>(kl, T, T_norm, loss_weight(tau, flags), loss);
+  if (!loss) return KD_OK;
+  mean_kernel<<<1, 1024, 0, s>>>(row, T, T_norm, loss_weight(tau, rt.flags), loss);
   count_launch();
   if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
   return KD_OK;
@@ -688,14 +720,14 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
 
 template <typename Elem>
 static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_norm, int64_t d,
-                          int64_t V, const float* t_vals, const int32_t* t_idx, int K,
-                          int64_t chunk, float tau, uint32_t flags, const float* lse,
-                          const float* grad_loss, void* dH, float* dW, int accumulate, void* ws,
+                          int64_t V, const RowTerms& rt, int64_t chunk, float tau,
+                          const float* lse, const float* grad_loss, void* dH, float* dW,
+                          int accumulate, void* ws,
                           cudaStream_t s, int num_sms, uint64_t limit_ns) {
   constexpr bool F32 = sizeof(Elem) == 4;
   constexpr int BK = ElemCfg<Elem>::BK;
   constexpr int INNER = ROW_BYTES / sizeof(Elem);
-  const WsLayout L = ws_layout(T, d, V, K, chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
+  const WsLayout L = ws_layout(T, d, V, rt.K, chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
   unsigned char* w = static_cast<unsigned char*>(ws);
   uint32_t* status = reinterpret_cast<uint32_t*>(w);
   int32_t* idx_s = reinterpret_cast<int32_t*>(w + L.idx_sorted);
@@ -705,19 +737,18 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
 
   if (cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return KD_ERR_CUDA;
   const float inv_tau = 1.f / tau;
-  if (launch_prep(t_vals, t_idx, T, K, V, inv_tau, (flags & KD_KL_LOGPROB_CACHE) ? 1 : 0, idx_s,
-                  p_s, stats, status, s, num_sms) != cudaSuccess)
+  if (launch_prep(rt, T, V, inv_tau, idx_s, p_s, stats, status, s, num_sms) != cudaSuccess)
     return KD_ERR_CUDA;
   CUtensorMap tW_k, tW_mn;
   if (!make_map(&tW_k, W, F32, d, V, d, BK, 128)) return KD_ERR_CUDA;     // [V, d], K = d
   if (!make_map(&tW_mn, W, F32, d, V, d, INNER, BK, true)) return KD_ERR_CUDA;  // K = V, N = d
   CUtensorMap tDW_out, tHP_out;
-  if (!make_out_map(&tDW_out, dW, true, d, V, d)) return KD_ERR_CUDA;
+  if (dW && !make_out_map(&tDW_out, dW, true, d, V, d)) return KD_ERR_CUDA;
   float* hpart = reinterpret_cast<float*>(w + L.hpart);
   if (!make_out_map(&tHP_out, hpart, true, d, KD_DH_MAX_SPLIT * L.rows_pad, d)) return KD_ERR_CUDA;
   const float zscale = 1.4426950408889634f * inv_tau;
   const float inv_T_tau =
-      static_cast<float>(loss_weight(tau, flags) / (static_cast<double>(T_norm) * tau));
+      static_cast<float>(loss_weight(tau, rt.flags) / (static_cast<double>(T_norm) * tau));
   // dz of KD_DW_GROUP consecutive chunks is kept side by side, so that dW is
   // updated once per group with K = the group's rows (halving dW's
   // read-modify-write traffic); dz and dH are formed chunk by chunk.
@@ -747,7 +778,7 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
       g.k_split = 1;
       g.row0 = c0;
       g.V = V;
-      g.Ktop = K;
+      g.Ktop = rt.K;
       g.zscale = zscale;
       g.idx_sorted = idx_s;
       g.p_sorted = p_s;
@@ -762,6 +793,7 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
       if (launch_gemm2<Elem, 0, 0, EPI_BWD_DZ>(tH_k, tW_k, tDz_out, g, s, num_sms) != cudaSuccess)
         return KD_ERR_CUDA;
 
+      if (!dH) continue;             // the caller wants dW alone
       // (2) dH_c = dz_c W : M = rows, N = d, K = V; A K-major, B MN-major;
       //     K split into even ranges whose fp32 partials are summed in order
       GemmArgs gh = g;
@@ -796,6 +828,7 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
       }
     }
 
+    if (!dW) continue;               // the caller wants dH alone (a frozen head)
     // (3) dW (+)= dz_g^T h_g over the group: M = V, N = d, K = grows; both
     //     operands MN-major
     const Elem* hg = static_cast<const Elem*>(h) + g0 * d;
@@ -826,26 +859,25 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
 }
 
 kd_status fused_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t T_norm, int64_t d,
-                    int64_t V, const float* t_vals, const int32_t* t_idx, int K, int64_t chunk,
-                    float tau, uint32_t flags, float* loss, float* lse, float* kl_rows, void* ws,
-                    cudaStream_t s, int num_sms, uint64_t limit_ns) {
+                    int64_t V, const RowTerms& rt, int64_t chunk, float tau, float* loss,
+                    float* lse, float* row_out, void* ws, cudaStream_t s, int num_sms,
+                    uint64_t limit_ns) {
   if (dtype == KD_DTYPE_F32)
-    return fwd_impl<float>(h, W, T, T_norm, d, V, t_vals, t_idx, K, chunk, tau, flags, loss, lse,
-                           kl_rows, ws, s, num_sms, limit_ns);
-  return fwd_impl<__nv_bfloat16>(h, W, T, T_norm, d, V, t_vals, t_idx, K, chunk, tau, flags, loss,
-                                 lse, kl_rows, ws, s, num_sms, limit_ns);
+    return fwd_impl<float>(h, W, T, T_norm, d, V, rt, chunk, tau, loss, lse, row_out, ws, s,
+                           num_sms, limit_ns);
+  return fwd_impl<__nv_bfloat16>(h, W, T, T_norm, d, V, rt, chunk, tau, loss, lse, row_out, ws, s,
+                                 num_sms, limit_ns);
 }
 
 kd_status fused_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t T_norm, int64_t d,
-                    int64_t V, const float* t_vals, const int32_t* t_idx, int K, int64_t chunk,
-                    float tau, uint32_t flags, const float* lse, const float* grad_loss, void* dH,
-                    float* dW, int accumulate, void* ws, cudaStream_t s, int num_sms,
-                    uint64_t limit_ns) {
+                    int64_t V, const RowTerms& rt, int64_t chunk, float tau, const float* lse,
+                    const float* grad_loss, void* dH, float* dW, int accumulate, void* ws,
+                    cudaStream_t s, int num_sms, uint64_t limit_ns) {
   if (dtype == KD_DTYPE_F32)
-    return bwd_impl<float>(h, W, T, T_norm, d, V, t_vals, t_idx, K, chunk, tau, flags, lse,
-                           grad_loss, dH, dW, accumulate, ws, s, num_sms, limit_ns);
-  return bwd_impl<__nv_bfloat16>(h, W, T, T_norm, d, V, t_vals, t_idx, K, chunk, tau, flags, lse,
-                                 grad_loss, dH, dW, accumulate, ws, s, num_sms, limit_ns);
+    return bwd_impl<float>(h, W, T, T_norm, d, V, rt, chunk, tau, lse, grad_loss, dH, dW,
+                           accumulate, ws, s, num_sms, limit_ns);
+  return bwd_impl<__nv_bfloat16>(h, W, T, T_norm, d, V, rt, chunk, tau, lse, grad_loss, dH, dW,
+                                 accumulate, ws, s, num_sms, limit_ns);
 }
 
 cudaError_t launch_wait_probe(uint32_t* status, uint64_t limit_ns, cudaStream_t s) {

@@ -8,7 +8,9 @@ missing or fails to load, every call raises.
 Low-level functions carry the C names (``kd_topk_build``, ``kd_fused_kl_fwd``,
 ``kd_fused_kl_bwd`` ...) and take raw integers (device pointers, sizes, stream
 handle).  ``topk_build``, ``fused_kl_fwd``, ``fused_kl_bwd`` and
-``FusedTopKKLLoss`` wrap them for torch tensors.
+``FusedTopKKLLoss`` wrap them for torch tensors, and so do ``head_logprobs``,
+``head_logprobs_bwd`` and ``HeadLogprobs`` for the log-probabilities of given
+tokens.
 """
 
 from __future__ import annotations
@@ -28,6 +30,7 @@ KD_OK, KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_WORKSPACE = 0, 1, 2, 3
 KD_ERR_BAD_INDEX, KD_ERR_TIMEOUT, KD_ERR_CUDA, KD_ERR_INTERNAL = 4, 5, 6, 7
 KD_DTYPE_F32, KD_DTYPE_BF16 = 0, 1
 KD_KL_LOGPROB_CACHE, KD_KL_TAU_SQUARED = 0x1, 0x2
+KD_TARGET_IGNORE = -100
 CACHE_KINDS = ("logits", "logprobs")
 
 _c_i64, _c_int, _c_sz, _c_vp, _c_u64 = ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_uint64
@@ -56,6 +59,12 @@ _SIGNATURES = {
     "kd_fused_kl_bwd_shard": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
                                        _c_int, _c_i64, ctypes.c_float, _c_u32, _c_i64, _c_vp, _c_vp,
                                        _c_vp, _c_vp, _c_int, _c_vp, _c_sz, _c_vp]),
+    "kd_head_logprob_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_int]),
+    "kd_head_logprob_fwd": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
+                                     ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
+    "kd_head_logprob_bwd": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
+                                     ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int,
+                                     _c_vp, _c_sz, _c_vp]),
     "kd_read_device_status": (_c_int, [_c_vp, _c_vp]),
     "kd_set_wait_limit_ns": (_c_int, [_c_u64]),
     "kd_debug_wait_probe": (_c_int, [_c_vp, _c_sz, _c_u64, _c_vp]),
@@ -179,6 +188,23 @@ def kd_fused_kl_fwd_noalloc(h, W, dtype, T, d, V, t_vals, t_idx, K, chunk, tempe
     array inside the library; see include/kd.h for its limit and caveats)."""
     return load().kd_fused_kl_fwd_noalloc(h, W, dtype, T, d, V, t_vals, t_idx, K, chunk, temperature,
                                           loss, lse, kl_rows, stream)
+
+
+def kd_head_logprob_workspace_size(T, d, V, chunk, dtype, backward):
+    return load().kd_head_logprob_workspace_size(T, d, V, chunk, dtype, backward)
+
+
+def kd_head_logprob_fwd(h, W, dtype, T, d, V, targets, chunk, temperature, logp, lse, ws, ws_bytes,
+                        stream):
+    return load().kd_head_logprob_fwd(h, W, dtype, T, d, V, targets, chunk, temperature, logp, lse,
+                                      ws, ws_bytes, stream)
+
+
+def kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse, grad_logp, grad_loss,
+                        dH, dW, accumulate_dW, ws, ws_bytes, stream):
+    return load().kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse,
+                                      grad_logp, grad_loss, dH, dW, accumulate_dW, ws, ws_bytes,
+                                      stream)
 
 
 def kd_read_device_status(ws, stream):
@@ -396,3 +422,126 @@ class FusedTopKKLLoss(torch.autograd.Function):
                                  grad_loss=g, ws=ctx.ws, cache=ctx.cache,
                                  tau_squared=ctx.tau_squared)
         return dH, dW.to(W.dtype), None, None, None, None, None, None
+
+
+# ------------------------------------------------- log-probabilities of given tokens
+
+def _require(name: str, t, dtype, shape, device):
+    """Checks one tensor argument: a dense CUDA tensor of this type and shape on
+    this device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a torch tensor is needed")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {dtype} is needed, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} is needed, not {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: on {t.device}, not on the CUDA device {device} of the call")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _use_stream(device, stream):
+    """Context in which a call's outputs and workspace are allocated and its
+    kernels launched: the given stream, or the device's current one."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _head_sizes(h, W, targets):
+    if not (isinstance(h, torch.Tensor) and isinstance(W, torch.Tensor)) or h.dim() != 2 or W.dim() != 2:
+        raise ValueError("h [T, d] and W [V, d] are needed")
+    T, d = h.shape
+    V = W.shape[0]
+    code = _dtype_code(h)
+    _require("h", h, h.dtype, (T, d), h.device)
+    _require("W", W, h.dtype, (V, d), h.device)
+    _require("targets", targets, torch.int32, (T,), h.device)
+    return T, d, V, code
+
+
+def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, stream=None,
+                  backward: bool = False):
+    """Log-probabilities of one token per position through the output head, the
+    [T, V] logits never materialised: (logp f32 [T], lse f32 [T], ws).
+
+    ``targets`` int32 [T]; KD_TARGET_IGNORE (-100) marks positions without a
+    token (logp 0, no gradient).  ``backward=True`` sizes the workspace for
+    ``head_logprobs_bwd`` as well, which takes ``lse`` and may take ``ws``."""
+    T, d, V, code = _head_sizes(h, W, targets)
+    with _use_stream(h.device, stream):
+        if ws is None:
+            ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, int(backward)),
+                                 h.device)
+        logp = torch.empty((T,), dtype=torch.float32, device=h.device)
+        lse = torch.empty((T,), dtype=torch.float32, device=h.device)
+        _check(kd_head_logprob_fwd(h.data_ptr(), W.data_ptr(), code, T, d, V, targets.data_ptr(),
+                                   chunk, float(temperature), logp.data_ptr(), lse.data_ptr(),
+                                   ws.data_ptr(), ws.numel(), _stream()),
+               "kd_head_logprob_fwd")
+    return logp, lse, ws
+
+
+def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: float = 1.0,
+                      grad_loss=None, ws=None, dH=None, dW=None, accumulate_dW: bool = False,
+                      stream=None, need=(True, True)):
+    """Gradients of sum_t grad_logp[t] * logp[t] (times the device scalar
+    ``grad_loss``): (dH [T, d] dtype of h, dW [V, d] f32, ws).  The logits are
+    recomputed chunk by chunk; ``accumulate_dW=True`` adds into a given dW.
+    ``need=(dH, dW)`` leaves out a gradient that is not wanted (None in its
+    place)."""
+    T, d, V, code = _head_sizes(h, W, targets)
+    _require("lse", lse, torch.float32, (T,), h.device)
+    _require("grad_logp", grad_logp, torch.float32, (T,), h.device)
+    if grad_loss is not None:
+        _require("grad_loss", grad_loss, torch.float32, grad_loss.shape, h.device)
+        if grad_loss.numel() != 1:
+            raise ValueError("grad_loss: one value is needed")
+    if accumulate_dW and dW is None:
+        raise ValueError("accumulate_dW: needs the dW to add to")
+    if not any(need):
+        raise ValueError("need: at least one gradient")
+    with _use_stream(h.device, stream):
+        if ws is None:
+            ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, 1), h.device)
+        if not need[0]:
+            dH = None
+        elif dH is None:
+            dH = torch.empty_like(h)
+        else:
+            _require("dH", dH, h.dtype, (T, d), h.device)
+        if not need[1]:
+            dW = None
+        elif dW is None:
+            dW = torch.empty((V, d), dtype=torch.float32, device=h.device)
+        else:
+            _require("dW", dW, torch.float32, (V, d), h.device)
+        _check(kd_head_logprob_bwd(h.data_ptr(), W.data_ptr(), code, T, d, V, targets.data_ptr(),
+                                   chunk, float(temperature), lse.data_ptr(), grad_logp.data_ptr(),
+                                   _ptr(grad_loss), _ptr(dH), _ptr(dW), int(accumulate_dW),
+                                   ws.data_ptr(), ws.numel(), _stream()),
+               "kd_head_logprob_bwd")
+    return dH, dW, ws
+
+
+class HeadLogprobs(torch.autograd.Function):
+    """``logp = HeadLogprobs.apply(h, W, targets, chunk, temperature)``: the
+    log-probabilities of ``head_logprobs`` with gradients to h and W (W's in
+    W's dtype)."""
+
+    @staticmethod
+    def forward(ctx, h, W, targets, chunk, temperature=1.0):
+        logp, lse, _ = head_logprobs(h, W, targets, chunk, temperature)
+        ctx.save_for_backward(h, W, targets, lse)
+        ctx.chunk, ctx.temperature = chunk, temperature
+        return logp
+
+    @staticmethod
+    def backward(ctx, g):
+        h, W, targets, lse = ctx.saved_tensors
+        dH, dW, _ = head_logprobs_bwd(h, W, targets, lse, g.contiguous(), ctx.chunk, ctx.temperature,
+                                      need=ctx.needs_input_grad[:2])
+        return dH, None if dW is None else dW.to(W.dtype), None, None, None

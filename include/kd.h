@@ -239,6 +239,50 @@ kd_status kd_fused_kl_bwd_shard(const void* h, const void* W, int dtype,
                                 void* dH, float* dW, int accumulate_dW,
                                 void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Log-probabilities of given tokens through the output head, with the same */
+/* chunked projection and recomputing backward as the KL loss: the scores    */
+/* that the policy and preference losses below are made of, and the way of   */
+/* their gradients back into h and W.                                        */
+/*   a = h W^T / tau,  LSE_t = log sum_v exp(a_tv),  logp_t = a_{t,y_t} - LSE_t */
+/* ------------------------------------------------------------------------ */
+
+/* A row with this target has no token: its logp is 0 and its gradient 0. */
+#define KD_TARGET_IGNORE (-100)
+
+/* Bytes of workspace: backward == 0 for kd_head_logprob_fwd alone (a fraction
+ * of what the backward needs), otherwise for both calls. */
+size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int dtype,
+                                      int backward);
+
+/*
+ * Forward.  h, W, dtype, T, d, V, chunk, temperature as for kd_fused_kl_fwd;
+ *   targets [T] int32: y_t in [0, V), or KD_TARGET_IGNORE
+ * Outputs (device): logp float32 [T], lse float32 [T] (of every row; keep it
+ * for the backward).  Bit-identical for every `chunk`.  A target outside [0, V)
+ * other than KD_TARGET_IGNORE is recorded as KD_ERR_BAD_INDEX; the outputs of
+ * that call are then unspecified.
+ */
+kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
+                              int64_t V, const int32_t* targets, int64_t chunk, float temperature,
+                              float* logp, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward for the gradient grad_logp [T] float32 of each row's log-probability
+ * (not read for ignored rows), times the device scalar grad_loss (NULL for 1):
+ *   dz_tv = g grad_logp_t / tau * ([v == y_t] - exp(a_tv - LSE_t))
+ *   dH = dz W -> [T, d], dtype of h (overwritten);  dW (+)= dz^T h -> [V, d]
+ *   float32, overwritten or (accumulate_dW != 0) added to.
+ * Either of dH and dW may be NULL: that gradient is not computed (a frozen head
+ * needs no dW).  dz is rounded to the operands' type, as in kd_fused_kl_bwd.  An ignored row
+ * contributes 0 times its h to dW, so h must be finite in every row.
+ */
+kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
+                              int64_t V, const int32_t* targets, int64_t chunk, float temperature,
+                              const float* lse, const float* grad_logp, const float* grad_loss,
+                              void* dH, float* dW, int accumulate_dW, void* ws, size_t ws_bytes,
+                              void* stream);
+
 /* Synchronises `stream`, then returns the device status recorded in `ws`
  * (KD_OK, KD_ERR_BAD_INDEX, KD_ERR_TIMEOUT or, in the debug build,
  * KD_ERR_INTERNAL), or KD_ERR_CUDA.  Works for the workspaces of both
