@@ -327,6 +327,148 @@ kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T
                        kd::wait_limit_ns());
 }
 
+// Layout checks shared by the objectives.
+static kd_status validate_layout(const int32_t* cu, int64_t n_seqs, int64_t n_tokens,
+                                 kd::SeqLayout* q) {
+  if (n_seqs < 1 || n_tokens < 1) return KD_ERR_INVALID_ARG;
+  if (!aligned(cu, 4) || (!cu && n_tokens % n_seqs != 0)) return KD_ERR_INVALID_ARG;
+  if (n_seqs > kd::OBJ_MAX_TOKENS || n_tokens > kd::OBJ_MAX_TOKENS) return KD_ERR_UNSUPPORTED;
+  q->cu = cu;
+  q->S = static_cast<int32_t>(n_seqs);
+  q->N = static_cast<int32_t>(n_tokens);
+  q->L = cu ? 0 : static_cast<int32_t>(n_tokens / n_seqs);
+  return KD_OK;
+}
+
+static size_t up1024(size_t x) { return (x + 1023) & ~size_t(1023); }
+
+size_t kd_policy_loss_workspace_size(int64_t n_seqs, int64_t n_tokens) {
+  if (n_seqs < 1 || n_tokens < 1 || n_seqs > kd::OBJ_MAX_TOKENS || n_tokens > kd::OBJ_MAX_TOKENS)
+    return 0;
+  return kd::OBJ_HEADER + up1024(4 * static_cast<size_t>(n_seqs)) +
+         kd::OBJ_MAX_BLOCKS * kd::OBJ_PARTIALS * sizeof(double);
+}
+
+kd_status kd_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
+                         const float* advantages, int advantages_per_token, const uint8_t* mask,
+                         const int32_t* cu_seqlens, int64_t n_seqs, int64_t n_tokens,
+                         double clip_low, double clip_high, double kl_coef, int reduction,
+                         double denom, float* loss, float* stats, float* dlogp, void* ws,
+                         size_t ws_bytes, void* stream) {
+  if (!logp || !advantages || !loss || !stats || !ws) return KD_ERR_INVALID_ARG;
+  if (!aligned(logp, 16) || !aligned(old_logp, 16) || !aligned(ref_logp, 16) ||
+      !aligned(advantages, advantages_per_token ? 16 : 4) || !aligned(mask, 16) ||
+      !aligned(loss, 4) || !aligned(stats, 4) || !aligned(dlogp, 16) || !aligned(ws, 1024))
+    return KD_ERR_INVALID_ARG;
+  if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0) || !isfinite(kl_coef) ||
+      (kl_coef != 0.0 && !ref_logp))
+    return KD_ERR_INVALID_ARG;
+  if (reduction != KD_REDUCE_TOKEN && reduction != KD_REDUCE_SEQUENCE &&
+      reduction != KD_REDUCE_FIXED)
+    return KD_ERR_INVALID_ARG;
+  if (reduction == KD_REDUCE_FIXED && !(denom > 0.0 && isfinite(denom))) return KD_ERR_INVALID_ARG;
+  kd::PolicyArgs a = {};
+  const kd_status st = validate_layout(cu_seqlens, n_seqs, n_tokens, &a.seq);
+  if (st != KD_OK) return st;
+  if (ws_bytes < kd_policy_loss_workspace_size(n_seqs, n_tokens)) return KD_ERR_WORKSPACE;
+  a.logp = logp;
+  a.old_logp = old_logp;
+  a.ref_logp = ref_logp;
+  a.adv = advantages;
+  a.mask = mask;
+  a.adv_per_token = advantages_per_token != 0;
+  a.reduction = reduction;
+  a.bound_hi = static_cast<float>(1.0 + clip_high);
+  a.bound_lo = static_cast<float>(1.0 - clip_low);
+  a.log_hi64 = log1p(clip_high);
+  a.log_lo64 = log1p(-clip_low);
+  a.log_hi = static_cast<float>(a.log_hi64);
+  a.log_lo = static_cast<float>(a.log_lo64);
+  a.kl_coef = static_cast<float>(kl_coef);
+  a.inv_denom = reduction == KD_REDUCE_FIXED ? static_cast<float>(1.0 / denom) : 0.f;
+  a.loss = loss;
+  a.stats = stats;
+  a.dlogp = dlogp;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  a.status = reinterpret_cast<uint32_t*>(w);
+  a.ticket = reinterpret_cast<uint32_t*>(w + 8);
+  a.count = reinterpret_cast<uint32_t*>(
+      w + (reduction == KD_REDUCE_SEQUENCE ? kd::OBJ_HEADER : 16));
+  a.partials = reinterpret_cast<double*>(w + kd::OBJ_HEADER +
+                                         up1024(4 * static_cast<size_t>(n_seqs)));
+  const int sms = num_sms_current();
+  if (sms <= 0) return KD_ERR_CUDA;
+  return kd::policy_loss(a, static_cast<cudaStream_t>(stream), sms);
+}
+
+size_t kd_preference_loss_workspace_size(int64_t n_pairs, int64_t n_tokens) {
+  if (n_pairs < 1 || n_tokens < 1 || n_pairs > kd::OBJ_MAX_TOKENS / 2 ||
+      n_tokens > kd::OBJ_MAX_TOKENS)
+    return 0;
+  const int64_t span = kd::pref_span(n_tokens);
+  const size_t spans = static_cast<size_t>((n_tokens + span - 1) / span);
+  const size_t S = 2 * static_cast<size_t>(n_pairs);
+  return kd::OBJ_HEADER + up1024(S * sizeof(kd::SeqPart)) + 2 * up1024(spans * sizeof(kd::SeqPart)) +
+         up1024(S * sizeof(float)) + kd::OBJ_MAX_BLOCKS * sizeof(double);
+}
+
+kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
+                             const int32_t* cu_seqlens, int64_t n_pairs, int64_t n_tokens,
+                             int kind, double beta, double margin, double label_smoothing,
+                             int length_normalize, int64_t pairs_total, float* loss,
+                             float* rewards, float* dlogp, void* ws, size_t ws_bytes,
+                             void* stream) {
+  if (!logp || !loss || !rewards || !ws) return KD_ERR_INVALID_ARG;
+  if (!aligned(logp, 16) || !aligned(ref_logp, 16) || !aligned(mask, 16) || !aligned(loss, 4) ||
+      !aligned(rewards, 4) || !aligned(dlogp, 16) || !aligned(ws, 1024))
+    return KD_ERR_INVALID_ARG;
+  if (kind != KD_PREF_SIGMOID && kind != KD_PREF_HINGE && kind != KD_PREF_IPO)
+    return KD_ERR_INVALID_ARG;
+  if (!(beta > 0.0 && isfinite(beta)) || !isfinite(margin) ||
+      !(label_smoothing >= 0.0 && label_smoothing < 0.5))
+    return KD_ERR_INVALID_ARG;
+  // a margin has no place in the squared form, label smoothing only in the logistic one
+  if ((kind == KD_PREF_IPO && margin != 0.0) || (kind != KD_PREF_SIGMOID && label_smoothing != 0.0))
+    return KD_ERR_INVALID_ARG;
+  if (n_pairs < 1 || pairs_total < n_pairs) return KD_ERR_INVALID_ARG;
+  if (n_pairs > kd::OBJ_MAX_TOKENS / 2) return KD_ERR_UNSUPPORTED;
+  kd::PrefArgs a = {};
+  const kd_status st = validate_layout(cu_seqlens, 2 * n_pairs, n_tokens, &a.seq);
+  if (st != KD_OK) return st;
+  if (ws_bytes < kd_preference_loss_workspace_size(n_pairs, n_tokens)) return KD_ERR_WORKSPACE;
+  a.logp = logp;
+  a.ref_logp = ref_logp;
+  a.mask = mask;
+  a.kind = kind;
+  a.normalize = length_normalize != 0;
+  a.beta = beta;
+  a.margin = margin;
+  a.smoothing = label_smoothing;
+  a.inv_pairs = 1.0 / static_cast<double>(pairs_total);
+  a.span = static_cast<int32_t>(kd::pref_span(n_tokens));
+  a.n_spans = (n_tokens + a.span - 1) / a.span;
+  a.loss = loss;
+  a.rewards = rewards;
+  a.dlogp = dlogp;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  const size_t S = 2 * static_cast<size_t>(n_pairs), part = sizeof(kd::SeqPart);
+  a.status = reinterpret_cast<uint32_t*>(w);
+  a.ticket = reinterpret_cast<uint32_t*>(w + 8);
+  w += kd::OBJ_HEADER;
+  a.whole = reinterpret_cast<kd::SeqPart*>(w);
+  w += up1024(S * part);
+  a.head = reinterpret_cast<kd::SeqPart*>(w);
+  w += up1024(static_cast<size_t>(a.n_spans) * part);
+  a.tail = reinterpret_cast<kd::SeqPart*>(w);
+  w += up1024(static_cast<size_t>(a.n_spans) * part);
+  a.coef = reinterpret_cast<float*>(w);
+  w += up1024(S * sizeof(float));
+  a.partials = reinterpret_cast<double*>(w);
+  const int sms = num_sms_current();
+  if (sms <= 0) return KD_ERR_CUDA;
+  return kd::preference_loss(a, static_cast<cudaStream_t>(stream), sms);
+}
+
 kd_status kd_read_device_status(const void* ws, void* stream) {
   if (!ws) return KD_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -84,6 +84,71 @@ cudaError_t launch_topk_bf16(const void* logits, int64_t T, int64_t V, int K, fl
                              int32_t* out_idx, uint32_t* status, unsigned long long* row_counter,
                              cudaStream_t stream, int num_sms);
 
+// ---- objectives over token log-probabilities (kd_objective.cu) ----
+
+// Sequences of tokens that lie one after the other: sequence b at
+// [cu[b], cu[b + 1]), or (cu null) rows of L tokens with N == S L.
+struct SeqLayout {
+  const int32_t* cu;
+  int32_t S, N, L;
+};
+
+// Largest number of tokens or sequences: the kernels' token offsets, with what
+// they read ahead of one, stay below 2^31.
+constexpr int64_t OBJ_MAX_TOKENS = (int64_t(1) << 31) - 1024;
+// First region of an objective's workspace: status word at byte 0, ticket of
+// the last block at byte 8, count of unmasked tokens at byte 16.
+constexpr size_t OBJ_HEADER = 1024;
+constexpr int64_t OBJ_MAX_BLOCKS = 2048;   // blocks that leave partial sums
+constexpr int OBJ_PARTIALS = 5;            // sums a block of the policy loss leaves
+
+struct PolicyArgs {
+  SeqLayout seq;
+  const float *logp, *old_logp, *ref_logp, *adv;
+  const uint8_t* mask;
+  int adv_per_token, reduction;
+  float bound_hi, bound_lo;         // 1 + clip_high, 1 - clip_low
+  float log_hi, log_lo;             // their logarithms, rounded, and exact:
+  double log_hi64, log_lo64;
+  float kl_coef, inv_denom;
+  float *loss, *stats, *dlogp;
+  uint32_t *status, *ticket, *count;
+  double* partials;
+};
+
+kd_status policy_loss(const PolicyArgs& a, cudaStream_t s, int num_sms);
+
+// What a span of tokens holds of a sequence: the sum and the number of its
+// unmasked tokens.
+struct SeqPart {
+  double sum, n;
+};
+
+struct PrefArgs {
+  SeqLayout seq;                    // S == 2 pairs: the chosen, then the rejected
+  const float *logp, *ref_logp;
+  const uint8_t* mask;
+  int kind, normalize;
+  double beta, margin, smoothing, inv_pairs;
+  int32_t span;                     // tokens a warp sums, a multiple of 128
+  int64_t n_spans;
+  float *loss, *rewards, *dlogp;
+  uint32_t *status, *ticket;
+  SeqPart *whole, *head, *tail;     // [S], [n_spans], [n_spans]
+  float* coef;                      // [S] gradient of each of a sequence's tokens
+  double* partials;
+};
+
+kd_status preference_loss(const PrefArgs& a, cudaStream_t s, int num_sms);
+
+// Tokens a warp sums: about one span for each of the warps that fill the
+// device, but whole rows of 128.
+constexpr int64_t PREF_WARPS = 148 * 48;
+inline int64_t pref_span(int64_t n_tokens) {
+  const int64_t rows = (n_tokens + 127) / 128;
+  return 128 * ((rows + PREF_WARPS - 1) / PREF_WARPS);
+}
+
 cudaError_t launch_wait_probe(uint32_t* status, uint64_t limit_ns, cudaStream_t s);
 
 // Current time limit of device-side waits (kd_set_wait_limit_ns).

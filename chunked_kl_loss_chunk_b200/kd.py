@@ -10,7 +10,8 @@ Low-level functions carry the C names (``kd_topk_build``, ``kd_fused_kl_fwd``,
 handle).  ``topk_build``, ``fused_kl_fwd``, ``fused_kl_bwd`` and
 ``FusedTopKKLLoss`` wrap them for torch tensors, and so do ``head_logprobs``,
 ``head_logprobs_bwd`` and ``HeadLogprobs`` for the log-probabilities of given
-tokens.
+tokens, and ``policy_loss``, ``PolicyLoss``, ``preference_loss`` and
+``PreferenceLoss`` for the objectives over them.
 """
 
 from __future__ import annotations
@@ -31,10 +32,14 @@ KD_ERR_BAD_INDEX, KD_ERR_TIMEOUT, KD_ERR_CUDA, KD_ERR_INTERNAL = 4, 5, 6, 7
 KD_DTYPE_F32, KD_DTYPE_BF16 = 0, 1
 KD_KL_LOGPROB_CACHE, KD_KL_TAU_SQUARED = 0x1, 0x2
 KD_TARGET_IGNORE = -100
+KD_REDUCE_TOKEN, KD_REDUCE_SEQUENCE, KD_REDUCE_FIXED = 0, 1, 2
+KD_PREF_SIGMOID, KD_PREF_HINGE, KD_PREF_IPO = 0, 1, 2
+REDUCTIONS = {"token": KD_REDUCE_TOKEN, "sequence": KD_REDUCE_SEQUENCE, "fixed": KD_REDUCE_FIXED}
+PREFERENCE_KINDS = {"sigmoid": KD_PREF_SIGMOID, "hinge": KD_PREF_HINGE, "ipo": KD_PREF_IPO}
 CACHE_KINDS = ("logits", "logprobs")
 
 _c_i64, _c_int, _c_sz, _c_vp, _c_u64 = ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_uint64
-_c_u32 = ctypes.c_uint32
+_c_u32, _c_f64 = ctypes.c_uint32, ctypes.c_double
 
 _SIGNATURES = {
     "kd_status_string": (ctypes.c_char_p, [_c_int]),
@@ -65,6 +70,13 @@ _SIGNATURES = {
     "kd_head_logprob_bwd": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
                                      ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int,
                                      _c_vp, _c_sz, _c_vp]),
+    "kd_policy_loss_workspace_size": (_c_sz, [_c_i64, _c_i64]),
+    "kd_policy_loss": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_i64, _c_i64, _c_f64,
+                                _c_f64, _c_f64, _c_int, _c_f64, _c_vp, _c_vp, _c_vp, _c_vp, _c_sz,
+                                _c_vp]),
+    "kd_preference_loss_workspace_size": (_c_sz, [_c_i64, _c_i64]),
+    "kd_preference_loss": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_f64, _c_f64,
+                                    _c_f64, _c_int, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
     "kd_read_device_status": (_c_int, [_c_vp, _c_vp]),
     "kd_set_wait_limit_ns": (_c_int, [_c_u64]),
     "kd_debug_wait_probe": (_c_int, [_c_vp, _c_sz, _c_u64, _c_vp]),
@@ -205,6 +217,30 @@ def kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse, 
     return load().kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse,
                                       grad_logp, grad_loss, dH, dW, accumulate_dW, ws, ws_bytes,
                                       stream)
+
+
+def kd_policy_loss_workspace_size(n_seqs, n_tokens):
+    return load().kd_policy_loss_workspace_size(n_seqs, n_tokens)
+
+
+def kd_policy_loss(logp, old_logp, ref_logp, advantages, advantages_per_token, mask, cu_seqlens,
+                   n_seqs, n_tokens, clip_low, clip_high, kl_coef, reduction, denom, loss, stats,
+                   dlogp, ws, ws_bytes, stream):
+    return load().kd_policy_loss(logp, old_logp, ref_logp, advantages, advantages_per_token, mask,
+                                 cu_seqlens, n_seqs, n_tokens, clip_low, clip_high, kl_coef,
+                                 reduction, denom, loss, stats, dlogp, ws, ws_bytes, stream)
+
+
+def kd_preference_loss_workspace_size(n_pairs, n_tokens):
+    return load().kd_preference_loss_workspace_size(n_pairs, n_tokens)
+
+
+def kd_preference_loss(logp, ref_logp, mask, cu_seqlens, n_pairs, n_tokens, kind, beta, margin,
+                       label_smoothing, length_normalize, pairs_total, loss, rewards, dlogp, ws,
+                       ws_bytes, stream):
+    return load().kd_preference_loss(logp, ref_logp, mask, cu_seqlens, n_pairs, n_tokens, kind, beta,
+                                     margin, label_smoothing, length_normalize, pairs_total, loss,
+                                     rewards, dlogp, ws, ws_bytes, stream)
 
 
 def kd_read_device_status(ws, stream):
@@ -545,3 +581,155 @@ class HeadLogprobs(torch.autograd.Function):
         dH, dW, _ = head_logprobs_bwd(h, W, targets, lse, g.contiguous(), ctx.chunk, ctx.temperature,
                                       need=ctx.needs_input_grad[:2])
         return dH, None if dW is None else dW.to(W.dtype), None, None, None
+
+
+# ------------------------------------------------- objectives over token log-probabilities
+
+def _sequences(logp, cu_seqlens, mask):
+    """(number of sequences, number of tokens) of a batch of token
+    log-probabilities: rows of a 2-D ``logp``, or ``cu_seqlens`` over a 1-D one."""
+    if not isinstance(logp, torch.Tensor):
+        raise TypeError("logp: a torch tensor is needed")
+    dev = logp.device
+    _require("logp", logp, torch.float32, logp.shape, dev)
+    if cu_seqlens is None:
+        if logp.dim() != 2:
+            raise ValueError("logp: [sequences, tokens] is needed, or cu_seqlens with one axis of tokens")
+        n_seqs = logp.shape[0]
+    else:
+        if logp.dim() != 1 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens: [sequences + 1] over one axis of tokens is needed")
+        _require("cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, dev)
+        n_seqs = cu_seqlens.shape[0] - 1
+    if mask is not None:
+        if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
+            raise TypeError(f"mask: bool or uint8 is needed, not {mask.dtype}")
+        _require("mask", mask, mask.dtype, logp.shape, dev)
+    return n_seqs, logp.numel()
+
+
+def _scratch(nbytes: int, device):
+    """Workspace of one call: (the buffer to keep, its aligned address, bytes)."""
+    n = max(int(nbytes), 1024)
+    buf = torch.empty(n + 1024, dtype=torch.uint8, device=device)
+    return buf, (buf.data_ptr() + 1023) & ~1023, n
+
+
+def policy_loss(logp, old_logp, advantages, *, mask=None, ref_logp=None, cu_seqlens=None,
+                advantages_per: str = "sequence", clip_low: float = 0.2, clip_high: float = 0.2,
+                kl_coef: float = 0.0, reduction: str = "token", denom: float | None = None,
+                grad: bool = True, ws=None, stream=None):
+    """Clipped policy loss with a KL term: (loss f32 [], stats f32 [4], dlogp f32
+    like logp, or None with ``grad=False``).
+
+    ``logp`` f32 [sequences, tokens], or [tokens] with ``cu_seqlens`` int32
+    [sequences + 1]; ``old_logp`` (None: on-policy, ratio 1) and ``ref_logp``
+    (None: no KL) like it; ``mask`` bool or uint8 like it; ``advantages`` f32
+    [sequences], or like ``logp`` with ``advantages_per="token"``.
+    ``reduction``: "token", "sequence" or "fixed" (with ``denom``).  ``stats``:
+    tokens that count, and over them the means of the ratio, of "clipped" and
+    of the KL estimate.  ``dlogp`` is what ``head_logprobs_bwd`` takes."""
+    n_seqs, n = _sequences(logp, cu_seqlens, mask)
+    dev = logp.device
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {tuple(REDUCTIONS)}")
+    if (reduction == "fixed") != (denom is not None):
+        raise ValueError("denom: belongs to reduction=\"fixed\" and to no other")
+    if advantages_per not in ("sequence", "token"):
+        raise ValueError("advantages_per must be \"sequence\" or \"token\"")
+    per_token = advantages_per == "token"
+    _require("advantages", advantages, torch.float32, logp.shape if per_token else (n_seqs,), dev)
+    if old_logp is not None:
+        _require("old_logp", old_logp, torch.float32, logp.shape, dev)
+    if ref_logp is not None:
+        _require("ref_logp", ref_logp, torch.float32, logp.shape, dev)
+    with _use_stream(dev, stream):
+        if ws is None:
+            keep, at, nbytes = _scratch(kd_policy_loss_workspace_size(n_seqs, n), dev)
+        else:
+            at, nbytes = ws.data_ptr(), ws.numel()
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        stats = torch.empty((4,), dtype=torch.float32, device=dev)
+        dlogp = torch.empty_like(logp) if grad else None
+        _check(kd_policy_loss(logp.data_ptr(), _ptr(old_logp), _ptr(ref_logp), advantages.data_ptr(),
+                              int(per_token), _ptr(mask), _ptr(cu_seqlens), n_seqs, n, clip_low,
+                              clip_high, kl_coef, REDUCTIONS[reduction],
+                              0.0 if denom is None else denom, loss.data_ptr(), stats.data_ptr(),
+                              _ptr(dlogp), at, nbytes, _stream()),
+               "kd_policy_loss")
+    return loss, stats, dlogp
+
+
+class PolicyLoss(torch.autograd.Function):
+    """``loss, stats = PolicyLoss.apply(logp, old_logp, advantages, options)``: the
+    loss of ``policy_loss`` with a gradient to ``logp``; ``options`` is a dict of
+    its keyword arguments."""
+
+    @staticmethod
+    def forward(ctx, logp, old_logp, advantages, options=None):
+        loss, stats, dlogp = policy_loss(logp, old_logp, advantages, **{
+            **(options or {}), "grad": ctx.needs_input_grad[0]})
+        ctx.save_for_backward(dlogp)
+        ctx.mark_non_differentiable(stats)
+        return loss, stats
+
+    @staticmethod
+    def backward(ctx, g, _):
+        (dlogp,) = ctx.saved_tensors
+        return dlogp * g, None, None, None
+
+
+def preference_loss(logp, *, ref_logp=None, mask=None, cu_seqlens=None, kind: str = "sigmoid",
+                    beta: float = 0.1, margin: float = 0.0, label_smoothing: float = 0.0,
+                    length_normalize: bool = False, pairs_total: int | None = None,
+                    grad: bool = True, ws=None, stream=None):
+    """Paired preference loss: (loss f32 [], rewards f32 [2 pairs], dlogp f32 like
+    logp, or None with ``grad=False``).
+
+    ``logp`` f32 [2 pairs, tokens], or [tokens] with ``cu_seqlens`` int32
+    [2 pairs + 1]: first every pair's chosen sequence, then every pair's rejected
+    one.  ``ref_logp`` (None: no reference) and ``mask`` like ``logp``.  ``kind``:
+    "sigmoid" (with ``label_smoothing``), "hinge" or "ipo".  ``pairs_total``: the
+    pairs of the whole batch when these are a part of it."""
+    n_seqs, n = _sequences(logp, cu_seqlens, mask)
+    dev = logp.device
+    if n_seqs % 2:
+        raise ValueError(f"{n_seqs} sequences: chosen and rejected ones come in pairs")
+    if kind not in PREFERENCE_KINDS:
+        raise ValueError(f"kind must be one of {tuple(PREFERENCE_KINDS)}")
+    if ref_logp is not None:
+        _require("ref_logp", ref_logp, torch.float32, logp.shape, dev)
+    pairs = n_seqs // 2
+    with _use_stream(dev, stream):
+        if ws is None:
+            keep, at, nbytes = _scratch(kd_preference_loss_workspace_size(pairs, n), dev)
+        else:
+            at, nbytes = ws.data_ptr(), ws.numel()
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        rewards = torch.empty((n_seqs,), dtype=torch.float32, device=dev)
+        dlogp = torch.empty_like(logp) if grad else None
+        _check(kd_preference_loss(logp.data_ptr(), _ptr(ref_logp), _ptr(mask), _ptr(cu_seqlens), pairs, n,
+                                  PREFERENCE_KINDS[kind], beta, margin, label_smoothing,
+                                  int(length_normalize), pairs if pairs_total is None else pairs_total,
+                                  loss.data_ptr(), rewards.data_ptr(), _ptr(dlogp), at, nbytes,
+                                  _stream()),
+               "kd_preference_loss")
+    return loss, rewards, dlogp
+
+
+class PreferenceLoss(torch.autograd.Function):
+    """``loss, rewards = PreferenceLoss.apply(logp, options)``: the loss of
+    ``preference_loss`` with a gradient to ``logp``; ``options`` is a dict of its
+    keyword arguments."""
+
+    @staticmethod
+    def forward(ctx, logp, options=None):
+        loss, rewards, dlogp = preference_loss(logp, **{**(options or {}), "grad": ctx.needs_input_grad[0]})
+        ctx.save_for_backward(dlogp)
+        ctx.mark_non_differentiable(rewards)
+        return loss, rewards
+
+    @staticmethod
+    def backward(ctx, g, _):
+        (dlogp,) = ctx.saved_tensors
+        return dlogp * g, None

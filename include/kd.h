@@ -283,10 +283,93 @@ kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T
                               void* dH, float* dW, int accumulate_dW, void* ws, size_t ws_bytes,
                               void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Objectives of post-training over the log-probabilities of a batch's      */
+/* tokens, each with its gradient for every token (what kd_head_logprob_bwd  */
+/* takes as grad_logp).                                                      */
+/*                                                                          */
+/* The batch is n_seqs sequences over n_tokens tokens, one after the other:  */
+/*   cu_seqlens int32 [n_seqs + 1] (device), 0 <= cu[0] <= ... <= cu[n_seqs]  */
+/*     <= n_tokens: sequence b is the tokens [cu[b], cu[b + 1]), and may be  */
+/*     empty; or NULL: rows of n_tokens / n_seqs tokens (no remainder).      */
+/*     Any other cu is recorded as KD_ERR_BAD_INDEX, with unspecified (but   */
+/*     in-bounds) outputs.                                                   */
+/*   mask [n_tokens], one byte a token, 0: the token does not count; NULL:   */
+/*     every token counts.  What the other arrays hold at a token that does  */
+/*     not count, or that lies outside every sequence, is never used (it may */
+/*     be NaN or infinite), and the token's gradient is written as 0.        */
+/* n_tokens and n_seqs are at most 2^31 - 1024 (KD_ERR_UNSUPPORTED).  Results */
+/* do not depend on timing: the same call gives the same bits.               */
+/* ------------------------------------------------------------------------ */
+
+/* What the sum over the tokens is divided by. */
+typedef enum kd_reduction {
+  KD_REDUCE_TOKEN = 0,    /* the number of tokens that count                           */
+  KD_REDUCE_SEQUENCE = 1, /* n_seqs, of each sequence's mean over its tokens that count */
+  KD_REDUCE_FIXED = 2     /* denom (a batch's number split over ranks or micro-batches) */
+} kd_reduction;
+
+size_t kd_policy_loss_workspace_size(int64_t n_seqs, int64_t n_tokens);
+
+/*
+ * Clipped policy loss with a KL term to a reference policy.  For a token of
+ * sequence b, with r = exp(logp - old_logp), q = ref_logp - logp and A its
+ * advantage:
+ *   loss_t = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A)
+ *            + kl_coef (exp(q) - 1 - q)
+ *   loss   = sum_t w_t loss_t,  w_t = 1 / count, 1 / (n_seqs count_b) or 1 / denom
+ *   dlogp_t = d loss / d logp_t    (0 through the clamp where it is active)
+ * Inputs (device, float32 [n_tokens] unless said otherwise):
+ *   logp        of the policy that is trained
+ *   old_logp    of the policy that sampled; NULL: logp itself, so r = 1
+ *   ref_logp    of the reference; NULL: no KL (kl_coef must then be 0)
+ *   advantages  [n_tokens] if advantages_per_token != 0, else [n_seqs]
+ *   clip_low in [0, 1], clip_high >= 0; denom > 0 for KD_REDUCE_FIXED only
+ * Outputs (device): loss float32 scalar; stats float32 [4]: the number of
+ * tokens that count, and over them the means of r, of "clipped" (r A above its
+ * clamped value) and of exp(q) - 1 - q; dlogp float32 [n_tokens], or NULL.
+ * Whether r is clipped is decided as in exact arithmetic.  With no token that
+ * counts, every output is 0; a sequence without one adds 0.
+ */
+kd_status kd_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
+                         const float* advantages, int advantages_per_token, const uint8_t* mask,
+                         const int32_t* cu_seqlens, int64_t n_seqs, int64_t n_tokens,
+                         double clip_low, double clip_high, double kl_coef, int reduction,
+                         double denom, float* loss, float* stats, float* dlogp, void* ws,
+                         size_t ws_bytes, void* stream);
+
+typedef enum kd_preference {
+  KD_PREF_SIGMOID = 0, /* -(1 - e) log sigmoid(z) - e log sigmoid(-z), e = label_smoothing */
+  KD_PREF_HINGE = 1,   /* max(0, 1 - z)                                                    */
+  KD_PREF_IPO = 2      /* (D - 1 / (2 beta))^2                                             */
+} kd_preference;
+
+size_t kd_preference_loss_workspace_size(int64_t n_pairs, int64_t n_tokens);
+
+/*
+ * Paired preference loss over 2 n_pairs sequences: pair i is sequence i
+ * (chosen) and sequence n_pairs + i (rejected).
+ *   s_b  = sum over b's tokens that count of (logp - ref_logp)   [ref NULL: logp]
+ *          divided by their number if length_normalize != 0 (0 without one)
+ *   D = s_i - s_{n_pairs + i},  z = beta D - margin
+ *   loss = (1 / pairs_total) sum_i of the kind's form of z or D
+ * Inputs (device): logp, ref_logp float32 [n_tokens].  beta > 0; margin 0 for
+ * KD_PREF_IPO; label_smoothing in [0, 1/2), 0 but for KD_PREF_SIGMOID;
+ * pairs_total >= n_pairs (the batch's pairs, when these are one shard of them).
+ * Outputs (device): loss float32 scalar; rewards float32 [2 n_pairs], beta s_b;
+ * dlogp float32 [n_tokens], or NULL.
+ */
+kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
+                             const int32_t* cu_seqlens, int64_t n_pairs, int64_t n_tokens,
+                             int kind, double beta, double margin, double label_smoothing,
+                             int length_normalize, int64_t pairs_total, float* loss,
+                             float* rewards, float* dlogp, void* ws, size_t ws_bytes,
+                             void* stream);
+
 /* Synchronises `stream`, then returns the device status recorded in `ws`
  * (KD_OK, KD_ERR_BAD_INDEX, KD_ERR_TIMEOUT or, in the debug build,
- * KD_ERR_INTERNAL), or KD_ERR_CUDA.  Works for the workspaces of both
- * kd_topk_build and the fused loss. */
+ * KD_ERR_INTERNAL), or KD_ERR_CUDA.  Works for the workspaces of every entry
+ * point above. */
 kd_status kd_read_device_status(const void* ws, void* stream);
 
 /* ------------------------------------------------------------------------ */
