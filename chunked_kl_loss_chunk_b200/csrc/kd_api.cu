@@ -469,6 +469,45 @@ kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uin
   return kd::preference_loss(a, static_cast<cudaStream_t>(stream), sms);
 }
 
+size_t kd_grad_clip_workspace_size(int n_tensors) {
+  if (n_tensors < 1) return 0;
+  return 1024 + (static_cast<size_t>(n_tensors) / kd::GRAD_MIN_TENSORS + 1) *
+                    static_cast<size_t>(kd::GRAD_MAX_BLOCKS) * sizeof(double);
+}
+
+kd_status kd_grad_sumsq(const void* const* grads, const int64_t* numels, const int* dtypes,
+                        int n_tensors, double* sumsq, void* ws, size_t ws_bytes, void* stream) {
+  if (!sumsq || !aligned(sumsq, 8) || !ws || !aligned(ws, 1024)) return KD_ERR_INVALID_ARG;
+  const kd::GradList l{grads, nullptr, numels, dtypes, n_tensors};
+  const kd_status st = kd::check_grads(l, false);
+  if (st != KD_OK) return st;
+  if (ws_bytes < kd_grad_clip_workspace_size(n_tensors)) return KD_ERR_WORKSPACE;
+  const int sms = num_sms_current();
+  if (sms <= 0) return KD_ERR_CUDA;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  return kd::grad_sumsq(l, sumsq, reinterpret_cast<uint32_t*>(w),
+                        reinterpret_cast<double*>(w + 1024), static_cast<cudaStream_t>(stream),
+                        sms);
+}
+
+kd_status kd_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                       const int* dtypes, int n_tensors, double max_norm, const double* sumsq,
+                       float* norm, void* ws, size_t ws_bytes, void* stream) {
+  if (!norm || !aligned(norm, 4) || !aligned(sumsq, 8) || !ws || !aligned(ws, 1024) ||
+      !(max_norm >= 0.0))
+    return KD_ERR_INVALID_ARG;
+  const kd::GradList l{grads, outs, numels, dtypes, n_tensors};
+  const kd_status st = kd::check_grads(l, true);
+  if (st != KD_OK) return st;
+  if (ws_bytes < kd_grad_clip_workspace_size(n_tensors)) return KD_ERR_WORKSPACE;
+  const int sms = num_sms_current();
+  if (sms <= 0) return KD_ERR_CUDA;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  return kd::grad_clip(l, max_norm, sumsq, norm, reinterpret_cast<uint32_t*>(w),
+                       reinterpret_cast<double*>(w + 1024), static_cast<cudaStream_t>(stream),
+                       sms);
+}
+
 kd_status kd_read_device_status(const void* ws, void* stream) {
   if (!ws) return KD_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

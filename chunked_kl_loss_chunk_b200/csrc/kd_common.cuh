@@ -308,4 +308,32 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// ----------------------------------------------------------------------------
+// fp64 sums in a fixed order.
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Sum over the block of N values per thread, in a fixed order; thread 0's
+// result is the sum.  `sm` holds N doubles per warp.
+template <int N>
+__device__ __forceinline__ void block_sum(double (&v)[N], double* sm) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nw = blockDim.x >> 5;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = warp_sum(v[i]);
+    if (lane == 0) sm[warp * N + i] = v[i];
+  }
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < nw ? sm[lane * N + i] : 0.0);
+  }
+  __syncthreads();
+}
+
 }  // namespace kd

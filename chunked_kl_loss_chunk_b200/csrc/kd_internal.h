@@ -149,6 +149,25 @@ inline int64_t pref_span(int64_t n_tokens) {
   return 128 * ((rows + PREF_WARPS - 1) / PREF_WARPS);
 }
 
+// ---- gradient norm and clipping (kd_gradnorm.cu) ----
+
+// Host arrays of n tensors; outs may be null where nothing is written.
+struct GradList {
+  const void* const* grads;
+  void* const* outs;
+  const int64_t* numels;
+  const int* dtypes;
+  int n;
+};
+constexpr int64_t GRAD_MAX_BLOCKS = 1024;      // sums that one launch leaves
+constexpr int GRAD_MIN_TENSORS = 1000;         // tensors a launch takes at least, but for the last
+
+kd_status check_grads(const GradList& l, bool writes);   // makes no CUDA call
+kd_status grad_sumsq(const GradList& l, double* sumsq, uint32_t* status, double* partials,
+                     cudaStream_t s, int num_sms);
+kd_status grad_clip(const GradList& l, double max_norm, const double* sumsq, float* norm,
+                    uint32_t* status, double* partials, cudaStream_t s, int num_sms);
+
 cudaError_t launch_wait_probe(uint32_t* status, uint64_t limit_ns, cudaStream_t s);
 
 // Current time limit of device-side waits (kd_set_wait_limit_ns).

@@ -83,3 +83,38 @@ def shard_step(h, W, t_vals, t_idx, T_total: int, chunk: int, temperature: float
         dist.all_reduce(dW, op=dist.ReduceOp.SUM, group=group)
         dist.all_reduce(loss, op=dist.ReduceOp.SUM, group=group)
     return loss.reshape(()), dH, dW
+
+
+def kd_clip_compute(grads, max_norm, sumsq=None):
+    """The sum of squares of `grads` (max_norm None), or their clipping in place
+    with a given one, in libkd's kernels."""
+    from chunked_kl_loss_chunk_b200 import kd
+    if max_norm is None:
+        return kd.grad_sumsq(grads)
+    return kd.clip_grad_norm(grads, max_norm, sumsq=sumsq)
+
+
+def clip_grad_norm(replicated, sharded, max_norm: float, *, compute: Callable = kd_clip_compute,
+                   group=None, device=None):
+    """Clips a data-parallel step's gradients in place to the norm over the whole
+    batch, and returns that norm (the same on every rank).
+
+    `replicated`: tensors that every rank holds alike (dW after ``shard_step``),
+    counted once; `sharded`: each rank's own rows (dH), whose sums of squares are
+    added over the ranks.  Either may be empty, also on some ranks only: every
+    rank joins the one all-reduce (of a fp64 scalar on `device`, by default the
+    tensors')."""
+    replicated = [t for t in replicated if t.numel()]
+    sharded = [t for t in sharded if t.numel()]
+    both = replicated + sharded
+    if device is None:
+        device = both[0].device if both else torch.device("cpu")
+    total = compute(sharded, None) if sharded else torch.zeros((), dtype=torch.float64, device=device)
+    world = dist.get_world_size(group) if dist.is_available() and dist.is_initialized() else 1
+    if world > 1:
+        dist.all_reduce(total, op=dist.ReduceOp.SUM, group=group)
+    if replicated:
+        total = total + compute(replicated, None)
+    if both:
+        return compute(both, max_norm, total)
+    return total.sqrt().to(torch.float32)

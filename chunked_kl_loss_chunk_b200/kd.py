@@ -11,11 +11,13 @@ handle).  ``topk_build``, ``fused_kl_fwd``, ``fused_kl_bwd`` and
 ``FusedTopKKLLoss`` wrap them for torch tensors, and so do ``head_logprobs``,
 ``head_logprobs_bwd`` and ``HeadLogprobs`` for the log-probabilities of given
 tokens, and ``policy_loss``, ``PolicyLoss``, ``preference_loss`` and
-``PreferenceLoss`` for the objectives over them.
+``PreferenceLoss`` for the objectives over them, ``grad_sumsq`` and
+``clip_grad_norm`` for the gradients of the whole step.
 """
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -77,6 +79,10 @@ _SIGNATURES = {
     "kd_preference_loss_workspace_size": (_c_sz, [_c_i64, _c_i64]),
     "kd_preference_loss": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_f64, _c_f64,
                                     _c_f64, _c_int, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
+    "kd_grad_clip_workspace_size": (_c_sz, [_c_int]),
+    "kd_grad_sumsq": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_sz, _c_vp]),
+    "kd_grad_clip": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_f64, _c_vp, _c_vp, _c_vp, _c_sz,
+                              _c_vp]),
     "kd_read_device_status": (_c_int, [_c_vp, _c_vp]),
     "kd_set_wait_limit_ns": (_c_int, [_c_u64]),
     "kd_debug_wait_probe": (_c_int, [_c_vp, _c_sz, _c_u64, _c_vp]),
@@ -241,6 +247,19 @@ def kd_preference_loss(logp, ref_logp, mask, cu_seqlens, n_pairs, n_tokens, kind
     return load().kd_preference_loss(logp, ref_logp, mask, cu_seqlens, n_pairs, n_tokens, kind, beta,
                                      margin, label_smoothing, length_normalize, pairs_total, loss,
                                      rewards, dlogp, ws, ws_bytes, stream)
+
+
+def kd_grad_clip_workspace_size(n_tensors):
+    return load().kd_grad_clip_workspace_size(n_tensors)
+
+
+def kd_grad_sumsq(grads, numels, dtypes, n_tensors, sumsq, ws, ws_bytes, stream):
+    return load().kd_grad_sumsq(grads, numels, dtypes, n_tensors, sumsq, ws, ws_bytes, stream)
+
+
+def kd_grad_clip(grads, outs, numels, dtypes, n_tensors, max_norm, sumsq, norm, ws, ws_bytes, stream):
+    return load().kd_grad_clip(grads, outs, numels, dtypes, n_tensors, max_norm, sumsq, norm, ws,
+                               ws_bytes, stream)
 
 
 def kd_read_device_status(ws, stream):
@@ -733,3 +752,65 @@ class PreferenceLoss(torch.autograd.Function):
     def backward(ctx, g, _):
         (dlogp,) = ctx.saved_tensors
         return dlogp * g, None
+
+
+# ------------------------------------------------- the gradients of the whole step
+
+_GRAD_CODES = {torch.float32: KD_DTYPE_F32, torch.bfloat16: KD_DTYPE_BF16}
+
+
+def _grad_arrays(name: str, tensors):
+    """Checks a list of gradients; (count, device, addresses, sizes, type codes)."""
+    n = len(tensors)
+    if n == 0:
+        raise ValueError(f"{name}: at least one tensor is needed")
+    try:
+        codes = [_GRAD_CODES[t.dtype] for t in tensors]
+    except (KeyError, AttributeError):
+        raise TypeError(f"{name}: float32 or bfloat16 tensors are needed") from None
+    device = tensors[0].device
+    if {t.get_device() for t in tensors} != {device.index} or device.type != "cuda":
+        raise ValueError(f"{name}: all tensors must be on one CUDA device")
+    if not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name}: must be contiguous")
+    return (n, device, array.array("Q", [t.data_ptr() for t in tensors]),
+            array.array("q", [t.numel() for t in tensors]), array.array("i", codes))
+
+
+def grad_sumsq(grads, stream=None):
+    """Sum of squares of a list of gradients, fp64 [] (its root is their norm)."""
+    grads = list(grads)
+    n, dev, ptrs, sizes, codes = _grad_arrays("grads", grads)
+    with _use_stream(dev, stream):
+        keep, at, nbytes = _scratch(kd_grad_clip_workspace_size(n), dev)
+        out = torch.empty((), dtype=torch.float64, device=dev)
+        _check(kd_grad_sumsq(ptrs.buffer_info()[0], sizes.buffer_info()[0], codes.buffer_info()[0], n,
+                             out.data_ptr(), at, nbytes, _stream()),
+               "kd_grad_sumsq")
+    return out
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, sumsq=None, stream=None):
+    """Scales a list of gradients by min(1, max_norm / (norm + 1e-6)), in place or
+    into the tensors of ``out`` (same sizes and types); returns the norm before
+    it, f32 [].  ``grads``: float32 and bfloat16 CUDA tensors of any shapes, each
+    contiguous.  ``sumsq`` fp64 []: the sum of squares to use, where the list is
+    a part of what the norm is taken over (``dp.clip_grad_norm``)."""
+    grads = list(grads)
+    n, dev, ptrs, sizes, codes = _grad_arrays("grads", grads)
+    outs = ptrs
+    if out is not None:
+        out = list(out)
+        m, out_dev, outs, out_sizes, out_codes = _grad_arrays("out", out)
+        if m != n or out_dev != dev or out_sizes != sizes or out_codes != codes:
+            raise ValueError("out: the sizes, types and device of grads are needed")
+    if sumsq is not None:
+        _require("sumsq", sumsq, torch.float64, (), dev)
+    with _use_stream(dev, stream):
+        keep, at, nbytes = _scratch(kd_grad_clip_workspace_size(n), dev)
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        _check(kd_grad_clip(ptrs.buffer_info()[0], outs.buffer_info()[0], sizes.buffer_info()[0],
+                            codes.buffer_info()[0], n, max_norm, _ptr(sumsq), norm.data_ptr(), at,
+                            nbytes, _stream()),
+               "kd_grad_clip")
+    return norm

@@ -366,6 +366,38 @@ kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uin
                              float* rewards, float* dlogp, void* ws, size_t ws_bytes,
                              void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The global norm of a list of gradients (dH, dW and whatever else the step */
+/* has), and clipping to it.  grads, outs, numels and dtypes are HOST arrays */
+/* of n_tensors >= 1 entries, read during the call (a captured graph keeps   */
+/* the addresses in them).  Tensors are dense, KD_DTYPE_F32 or KD_DTYPE_BF16,*/
+/* may be empty (numels 0), and need only the alignment of their elements:   */
+/* views into a flat buffer will do.                                         */
+/* ------------------------------------------------------------------------ */
+
+size_t kd_grad_clip_workspace_size(int n_tensors);
+
+/* *sumsq (device, double) = the sum of squares of all elements, added in fp64
+ * in an order that depends on the sizes alone.  For norms over several ranks:
+ * add the ranks' sums of the tensors that are split, then call kd_grad_clip. */
+kd_status kd_grad_sumsq(const void* const* grads, const int64_t* numels, const int* dtypes,
+                        int n_tensors, double* sumsq, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ *   x = sqrt(sum of squares),  c = min(1, max_norm / (x + 1e-6)),  out = c grad
+ * outs[i] has grads[i]'s size and type; it is grads[i] itself (clipping in
+ * place, which writes nothing where c is 1), or shares no memory with any other
+ * tensor of the list (KD_ERR_INVALID_ARG otherwise: the same gradient twice in
+ * an in-place list would be scaled twice).  sumsq (device, or NULL: computed
+ * from grads) is the sum of squares to use.  *norm (device, float32) = x.
+ * max_norm >= 0; infinite: c is 1, the norm alone is wanted.  A norm that is
+ * infinite or NaN makes c 0 or NaN, as the formula says.
+ * KD_ERR_INTERNAL: the host had no memory for checking the list.
+ */
+kd_status kd_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                       const int* dtypes, int n_tensors, double max_norm, const double* sumsq,
+                       float* norm, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then returns the device status recorded in `ws`
  * (KD_OK, KD_ERR_BAD_INDEX, KD_ERR_TIMEOUT or, in the debug build,
  * KD_ERR_INTERNAL), or KD_ERR_CUDA.  Works for the workspaces of every entry

@@ -107,3 +107,47 @@ def test_python_refusals_without_a_gpu():
     for call in (lambda: kd.policy_loss(x, x, a), lambda: kd.preference_loss(x)):
         with pytest.raises(ValueError, match="CUDA device"):      # there is no CPU fallback
             call()
+
+
+def _clip(n=2, grads=(FAKE, FAKE + 4096), outs=(FAKE, FAKE + 4096), sizes=(100, 7), types=(0, 1), max_norm=1.0,
+          sumsq=None, norm=FAKE, ws=FAKE, ws_bytes=1 << 40, what="clip"):
+    import ctypes
+    arr = lambda t, v: None if v is None else (t * max(len(v), 1))(*v)  # noqa: E731
+    g, o = arr(ctypes.c_void_p, grads), arr(ctypes.c_void_p, outs)
+    s, t = arr(ctypes.c_int64, sizes), arr(ctypes.c_int, types)
+    if what == "sumsq":
+        return kd.kd_grad_sumsq(g, s, t, n, norm, ws, ws_bytes, None)
+    return kd.kd_grad_clip(g, o, s, t, n, max_norm, sumsq, norm, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("what", ["clip", "sumsq"])
+def test_grad_refusals(what):
+    for kw in (dict(n=0), dict(n=-1), dict(grads=None), dict(sizes=None), dict(types=None), dict(norm=None),
+               dict(norm=FAKE + 2), dict(ws=None), dict(ws=FAKE + 512), dict(sizes=(100, -1)),
+               dict(grads=(None, FAKE), outs=(FAKE + 64, FAKE)), dict(grads=(FAKE + 2, FAKE + 4096)),
+               dict(grads=(FAKE, FAKE + 4097))):
+        assert _clip(what=what, **kw) == kd.KD_ERR_INVALID_ARG, kw
+    assert _clip(what=what, types=(0, 2)) == kd.KD_ERR_UNSUPPORTED
+    assert _clip(what=what, sizes=(1 << 40, 7), outs=(FAKE, FAKE)) == kd.KD_ERR_UNSUPPORTED
+    assert _clip(what=what, ws_bytes=1024) == kd.KD_ERR_WORKSPACE
+    assert kd.kd_grad_clip_workspace_size(0) == 0
+    assert kd.kd_grad_clip_workspace_size(5000) > kd.kd_grad_clip_workspace_size(999)
+
+
+def test_grad_clip_refuses_shared_memory():
+    bad = kd.KD_ERR_INVALID_ARG
+    far = FAKE + (1 << 20)
+    for kw in (dict(max_norm=-1.0), dict(max_norm=math.nan), dict(outs=None), dict(outs=(None, FAKE)),
+               dict(sumsq=FAKE + 4), dict(outs=(FAKE + 2, FAKE + 4096)),
+               dict(grads=(FAKE, FAKE), outs=(FAKE, FAKE)),                         # the same one twice
+               dict(grads=(FAKE, FAKE + 396), outs=(FAKE, FAKE + 396)),             # the last 4 bytes
+               dict(grads=(FAKE, far), outs=(far, FAKE)),                           # exchanged
+               dict(grads=(FAKE, far), outs=(far + 12, far + 64)),                  # an output on a gradient
+               dict(grads=(FAKE, far), outs=(FAKE + 4, far)),                       # on its own, shifted
+               dict(grads=(FAKE, far), outs=(far + 4096, far + 4096 + 398))):       # two outputs
+        assert _clip(**kw) == bad, kw
+    # what only touches, and gradients that share memory but are only read, pass on to the next check
+    for kw in (dict(grads=(FAKE, FAKE + 400), outs=(FAKE, FAKE + 400)),
+               dict(grads=(FAKE, FAKE + 4), outs=(far, far + 400)),
+               dict(grads=(FAKE, FAKE), outs=(FAKE, FAKE), sizes=(100, 0))):
+        assert _clip(ws_bytes=16, **kw) == kd.KD_ERR_WORKSPACE, kw
