@@ -1,0 +1,67 @@
+"""Post-training steps through the output head: tokens in, gradients of h and W out.
+
+What follows distillation trains the same head on sampled or compared answers.
+A step is three calls of ``kd``: the log-probabilities of the answers' tokens
+(``head_logprobs``), an objective over them with its gradient for each token
+(``policy_loss`` or ``preference_loss``), and the way of that gradient back into
+h and W (``head_logprobs_bwd``); the [T, V] logits are never materialised, and
+one workspace serves both passes through the head.  ``kd.clip_grad_norm`` (or
+``dp.clip_grad_norm`` over ranks) then clips the step's gradients.
+
+Nothing synchronises, so a step can be captured in a CUDA graph.
+"""
+
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from chunked_kl_loss_chunk_b200 import kd
+
+
+class Step(NamedTuple):
+    loss: torch.Tensor        # f32 []
+    extra: torch.Tensor       # policy_step: stats f32 [4]; preference_step: rewards f32 [2 pairs]
+    logp: torch.Tensor        # f32, like targets
+    dH: torch.Tensor          # [T, d], dtype of h
+    dW: torch.Tensor          # [V, d] f32
+    ws: torch.Tensor          # the head's workspace, for kd.read_device_status or the next step
+
+
+def _through_head(h, W, targets, objective, chunk, temperature, ws, dW, accumulate_dW):
+    flat = targets.reshape(-1)
+    logp, lse, ws = kd.head_logprobs(h, W, flat, chunk, temperature, ws=ws, backward=True)
+    logp = logp.view(targets.shape)
+    loss, extra, dlogp = objective(logp, targets != kd.KD_TARGET_IGNORE)
+    dH, dW, _ = kd.head_logprobs_bwd(h, W, flat, lse, dlogp.view(-1), chunk, temperature, ws=ws, dW=dW,
+                                     accumulate_dW=accumulate_dW)
+    return Step(loss, extra, logp, dH, dW, ws)
+
+
+def policy_step(h, W, targets, old_logp, advantages, *, chunk: int, temperature: float = 1.0, ref_logp=None,
+                cu_seqlens=None, ws=None, dW=None, accumulate_dW: bool = False, **options) -> Step:
+    """Clipped policy loss of sampled answers and its gradients.
+
+    h [T, d], W [V, d]; ``targets`` int32 [sequences, tokens], or [T] with
+    ``cu_seqlens``: the sampled token at each position, KD_TARGET_IGNORE where
+    there is none (prompts, padding), which is also the loss's mask.
+    ``old_logp``, ``ref_logp`` like ``targets``; ``options`` go to
+    ``kd.policy_loss`` (clip_low, clip_high, kl_coef, reduction, denom,
+    advantages_per).  For micro-batches, ``reduction="fixed"`` with the batch's
+    token count and ``accumulate_dW=True`` add up to the batch's gradient."""
+    return _through_head(h, W, targets, lambda logp, mask: kd.policy_loss(
+        logp, old_logp, advantages, mask=mask, ref_logp=ref_logp, cu_seqlens=cu_seqlens, **options),
+        chunk, temperature, ws, dW, accumulate_dW)
+
+
+def preference_step(h, W, targets, *, chunk: int, temperature: float = 1.0, ref_logp=None, cu_seqlens=None,
+                    ws=None, dW=None, accumulate_dW: bool = False, **options) -> Step:
+    """Paired preference loss of compared answers and its gradients.
+
+    ``targets`` as for ``policy_step``, over 2 pairs sequences: the chosen
+    answers, then the rejected ones.  ``options`` go to ``kd.preference_loss``
+    (kind, beta, margin, label_smoothing, length_normalize, pairs_total)."""
+    return _through_head(h, W, targets, lambda logp, mask: kd.preference_loss(
+        logp, ref_logp=ref_logp, mask=mask, cu_seqlens=cu_seqlens, **options),
+        chunk, temperature, ws, dW, accumulate_dW)
