@@ -209,7 +209,7 @@ static kd_status bwd_entry(const void* h, const void* W, int dtype, int64_t T, i
   rt.K = K;
   rt.flags = flags;
   return kd::fused_bwd(h, W, dtype, T, T_norm, d, V, rt, chunk, temperature, lse, grad_loss, dH, dW,
-                       accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
+                       KD_DTYPE_F32, accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
                        kd::wait_limit_ns());
 }
 
@@ -268,25 +268,34 @@ kd_status kd_fused_kl_bwd_shard(const void* h, const void* W, int dtype, int64_t
                    grad_loss, dH, dW, accumulate_dW, ws, ws_bytes, stream);
 }
 
+static int64_t head_fwd_chunk(int64_t chunk) {
+  return chunk > kd::KD_HEAD_FWD_ROWS ? chunk : kd::KD_HEAD_FWD_ROWS;
+}
+
 size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int dtype,
                                       int backward) {
   if (T < 1 || d < 1 || V < 1 || chunk < 1) return 0;
+  const kd::WsLayout F = kd::ws_layout(T, d, V, 1, head_fwd_chunk(chunk), dtype);
+  if (!F.ok) return 0;
+  if (!backward) return F.fwd_end;
   const kd::WsLayout L = kd::ws_layout(T, d, V, 1, chunk, dtype);
-  return L.ok ? (backward ? L.total : L.fwd_end) : 0;
+  if (!L.ok) return 0;
+  return L.total > F.fwd_end ? L.total : F.fwd_end;
 }
 
-// Checks shared by the two calls below; `need` is WsLayout::fwd_end or ::total.
+// Checks shared by the two calls below.
 static kd_status validate_head(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                                int64_t V, const int32_t* targets, int64_t chunk, float tau,
-                               void* ws, size_t ws_bytes, size_t kd::WsLayout::*need) {
+                               void* ws, size_t ws_bytes, bool backward) {
   // one entry per row: `targets` stands in for both arrays of a cache with K = 1
   const kd_status st =
       kd::validate_loss_inputs(h, W, dtype, T, d, V, reinterpret_cast<const float*>(targets),
                                targets, 1, chunk, tau);
   if (st != KD_OK) return st;
   if (!ws || !aligned(ws, kd::KD_WS_ALIGN)) return KD_ERR_INVALID_ARG;
-  const kd::WsLayout L = kd::ws_layout(T, d, V, 1, chunk, dtype);
-  if (!L.ok || ws_bytes < L.*need) return KD_ERR_WORKSPACE;
+  const kd::WsLayout L =
+      kd::ws_layout(T, d, V, 1, backward ? chunk : head_fwd_chunk(chunk), dtype);
+  if (!L.ok || ws_bytes < (backward ? L.total : L.fwd_end)) return KD_ERR_WORKSPACE;
   return KD_OK;
 }
 
@@ -294,36 +303,40 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
                               float* logp, float* lse, void* ws, size_t ws_bytes, void* stream) {
   const kd_status st = validate_head(h, W, dtype, T, d, V, targets, chunk, temperature, ws,
-                                     ws_bytes, &kd::WsLayout::fwd_end);
+                                     ws_bytes, false);
   if (st != KD_OK) return st;
   if (!logp || !lse || !aligned(logp, 16) || !aligned(lse, 16)) return KD_ERR_INVALID_ARG;
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
   kd::RowTerms rt;
   rt.targets = targets;
-  return kd::fused_fwd(h, W, dtype, T, 1, d, V, rt, chunk, temperature, nullptr, lse, logp, ws,
-                       static_cast<cudaStream_t>(stream), sms, kd::wait_limit_ns());
+  return kd::fused_fwd(h, W, dtype, T, 1, d, V, rt, head_fwd_chunk(chunk), temperature, nullptr,
+                       lse, logp, ws, static_cast<cudaStream_t>(stream), sms, kd::wait_limit_ns());
 }
 
 kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
                               const float* lse, const float* grad_logp, const float* grad_loss,
-                              void* dH, float* dW, int accumulate_dW, void* ws, size_t ws_bytes,
-                              void* stream) {
+                              void* dH, void* dW, int dW_dtype, int accumulate_dW, void* ws,
+                              size_t ws_bytes, void* stream) {
   const kd_status st = validate_head(h, W, dtype, T, d, V, targets, chunk, temperature, ws,
-                                     ws_bytes, &kd::WsLayout::total);
+                                     ws_bytes, true);
   if (st != KD_OK) return st;
   if (!lse || !grad_logp || (!dH && !dW)) return KD_ERR_INVALID_ARG;
   if (!aligned(lse, 16) || !aligned(grad_logp, 16) || !aligned(dH, 16) || !aligned(dW, 16) ||
       (grad_loss && !aligned(grad_loss, 4)))
     return KD_ERR_INVALID_ARG;
+  if (dW && dW_dtype != KD_DTYPE_F32 &&
+      (dW_dtype != KD_DTYPE_BF16 || dtype != KD_DTYPE_BF16 || accumulate_dW ||
+       (T + kd::KD_DW_GROUP - 1) / kd::KD_DW_GROUP > chunk))
+    return KD_ERR_UNSUPPORTED;
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
   kd::RowTerms rt;
   rt.targets = targets;
   rt.grad_rows = grad_logp;
   return kd::fused_bwd(h, W, dtype, T, 1, d, V, rt, chunk, temperature, lse, grad_loss, dH, dW,
-                       accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
+                       dW ? dW_dtype : KD_DTYPE_F32, accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
                        kd::wait_limit_ns());
 }
 

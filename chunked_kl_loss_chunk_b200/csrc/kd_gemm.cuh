@@ -48,7 +48,7 @@ struct ElemCfg<float> {
 enum EpiKind : int {
   EPI_FWD_LSE = 0,        // logsumexp / gather partials per (row, vocabulary tile)
   EPI_BWD_DZ = 1,         // dz boxes
-  EPI_STORE_H = 2,        // dH boxes in the dtype of h
+  EPI_STORE_W = 2,        // dW boxes in the operands' dtype, stored
   EPI_ACCUM_W = 3,        // fp32 dW boxes, stored or added
   EPI_STORE_PARTIAL = 4   // fp32 boxes of one K-split's partial dH
 };
@@ -149,8 +149,8 @@ __device__ __forceinline__ int lower_bound_i32(const int32_t* ids, int K, int32_
 // of tcgen05.ld (they are warp-collective).
 // ----------------------------------------------------------------------------
 template <typename Elem, int EPI>
-// pace_ns (EPI_ACCUM_W): pause between two output boxes of a warp, so that a
-// tile's fp32 dW boxes go out spread over the next tile's mainloop.
+// pace_ns (dW): pause between two output boxes of a warp, so that a
+// tile's dW boxes go out spread over the next tile's mainloop.
 __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMap* tmC, int m_base,
                                              int nb, uint32_t taddr, int quad, int lane,
                                              unsigned char* boxes, int y_extra = 0,
@@ -248,7 +248,7 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
       }
       KD_CHECK(!row_ok || static_cast<int64_t>(nidx) >= (n0 + BN < g.V ? n0 + BN : g.V), g.status);
     }
-  } else {  // EPI_STORE_H (dtype of h), EPI_STORE_PARTIAL (fp32) or EPI_ACCUM_W (fp32)
+  } else {  // EPI_STORE_W (Elem), EPI_STORE_PARTIAL (fp32) or EPI_ACCUM_W (fp32)
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
       const int base = n0 + c * 32;
@@ -257,10 +257,10 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
       box_reuse_wait();
       float v[32];
       tmem_ld32(taddr + c * 32, v);
-      if constexpr (EPI == EPI_STORE_H && sizeof(Elem) == 2) stage_box_bf16(box, lane, v);
+      if constexpr (EPI == EPI_STORE_W && sizeof(Elem) == 2) stage_box_bf16(box, lane, v);
       else stage_box_f32(box, lane, v);
       emit_box<Elem>(tmC, box, base, y_box, EPI == EPI_ACCUM_W && g.accumulate);
-      if (EPI == EPI_ACCUM_W && pace_ns) __nanosleep(pace_ns);
+      if ((EPI == EPI_ACCUM_W || EPI == EPI_STORE_W) && pace_ns) __nanosleep(pace_ns);
     }
   }
 }

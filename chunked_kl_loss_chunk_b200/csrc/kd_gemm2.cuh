@@ -217,7 +217,8 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
   // call's first kernel (launched in plain stream order) started, so their
   // loads need not wait: the mainloop of the first tiles overlaps the tail of
   // the kernel before.
-  constexpr bool kOperandsWait = (EPI == EPI_STORE_PARTIAL || EPI == EPI_ACCUM_W);
+  constexpr bool kIsDW = (EPI == EPI_ACCUM_W || EPI == EPI_STORE_W);
+  constexpr bool kOperandsWait = (EPI == EPI_STORE_PARTIAL || kIsDW);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
@@ -353,7 +354,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
       walk_check(w, g, m_tiles2);
       if (!mbar_wait(&tfull[acc], acc_phase, g.wait_limit_ns, g.status)) break;
       tc_fence_after();
-      if (EPI == EPI_ACCUM_W) {
+      if (kIsDW) {
         if (lane == 0) {
           const uint64_t now = globaltimer_ns();
           if (prev_ready != 0) {

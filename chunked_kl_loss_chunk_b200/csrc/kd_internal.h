@@ -65,7 +65,8 @@ struct RowTerms {
 // The fused loss over T positions whose loss and gradients are normalised by
 // T_norm >= T: T_norm == T for a whole batch, the batch's total positions when
 // these T rows are one data-parallel shard of it (then the shards' losses and
-// dW contributions sum to the batch's).  Log-probabilities of targets pass
+// dW contributions sum to the batch's).  dW is fp32, or for bf16 operands, with
+// T <= KD_DW_GROUP chunk and accumulate == 0, dW_dtype KD_DTYPE_BF16.  Log-probabilities of targets pass
 // T_norm == 1, and loss == null (no mean is taken).  row_out: KL_t or logp_t.
 kd_status fused_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t T_norm, int64_t d,
                     int64_t V, const RowTerms& rt, int64_t chunk, float tau, float* loss,
@@ -74,8 +75,14 @@ kd_status fused_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t 
 
 kd_status fused_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t T_norm, int64_t d,
                     int64_t V, const RowTerms& rt, int64_t chunk, float tau, const float* lse,
-                    const float* grad_loss, void* dH, float* dW, int accumulate, void* ws,
-                    cudaStream_t s, int num_sms, uint64_t limit_ns);
+                    const float* grad_loss, void* dH, void* dW, int dW_dtype, int accumulate,
+                    void* ws, cudaStream_t s, int num_sms, uint64_t limit_ns);
+
+// Rows that one launch of the head's log-probability forward takes at least: what
+// it keeps of a row is 16 bytes per 256 vocabulary entries (17 MB at this many
+// rows and V = 131072), so a smaller chunk, which bounds the backward's dz, would
+// only cost launches.
+constexpr int64_t KD_HEAD_FWD_ROWS = 2048;
 
 // The top-K build's workspace: the status word at byte 0 and the row counter
 // (zero before each build) at byte 8.

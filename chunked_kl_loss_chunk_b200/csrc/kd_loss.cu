@@ -538,7 +538,7 @@ int max_pair_clusters(Kern kern, int num_sms) {
 template <typename Elem, int A_MN, int B_MN, int EPI>
 cudaError_t launch_gemm2(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                          GemmArgs g, cudaStream_t s, int num_sms) {
-  static constexpr int kKind[5] = {KD_GEMM_FWD_LSE, KD_GEMM_BWD_DZ, KD_GEMM_DH, KD_GEMM_DW,
+  static constexpr int kKind[5] = {KD_GEMM_FWD_LSE, KD_GEMM_BWD_DZ, KD_GEMM_DW, KD_GEMM_DW,
                                    KD_GEMM_DH};
   auto kern = gemm2_kernel<Elem, A_MN, B_MN, EPI>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -721,8 +721,8 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
 template <typename Elem>
 static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_norm, int64_t d,
                           int64_t V, const RowTerms& rt, int64_t chunk, float tau,
-                          const float* lse, const float* grad_loss, void* dH, float* dW,
-                          int accumulate, void* ws,
+                          const float* lse, const float* grad_loss, void* dH, void* dW,
+                          int dW_dtype, int accumulate, void* ws,
                           cudaStream_t s, int num_sms, uint64_t limit_ns) {
   constexpr bool F32 = sizeof(Elem) == 4;
   constexpr int BK = ElemCfg<Elem>::BK;
@@ -743,7 +743,7 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   if (!make_map(&tW_k, W, F32, d, V, d, BK, 128)) return KD_ERR_CUDA;     // [V, d], K = d
   if (!make_map(&tW_mn, W, F32, d, V, d, INNER, BK, true)) return KD_ERR_CUDA;  // K = V, N = d
   CUtensorMap tDW_out, tHP_out;
-  if (dW && !make_out_map(&tDW_out, dW, true, d, V, d)) return KD_ERR_CUDA;
+  if (dW && !make_out_map(&tDW_out, dW, dW_dtype == KD_DTYPE_F32, d, V, d)) return KD_ERR_CUDA;
   float* hpart = reinterpret_cast<float*>(w + L.hpart);
   if (!make_out_map(&tHP_out, hpart, true, d, KD_DH_MAX_SPLIT * L.rows_pad, d)) return KD_ERR_CUDA;
   const float zscale = 1.4426950408889634f * inv_tau;
@@ -851,9 +851,12 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
     gw.accumulate = (accumulate || g0 > 0) ? 1 : 0;
     gw.status = status;
     gw.wait_limit_ns = limit_ns;
-    if (launch_gemm2<Elem, 1, 1, EPI_ACCUM_W>(tDz_mn, tH_mn, tDW_out, gw, s, num_sms) !=
-        cudaSuccess)
-      return KD_ERR_CUDA;
+    cudaError_t e = cudaErrorInvalidValue;
+    if (dW_dtype == KD_DTYPE_F32)
+      e = launch_gemm2<Elem, 1, 1, EPI_ACCUM_W>(tDz_mn, tH_mn, tDW_out, gw, s, num_sms);
+    else if constexpr (!F32)        // one group: nothing to add to
+      e = launch_gemm2<Elem, 1, 1, EPI_STORE_W>(tDz_mn, tH_mn, tDW_out, gw, s, num_sms);
+    if (e != cudaSuccess) return KD_ERR_CUDA;
   }
   return KD_OK;
 }
@@ -871,13 +874,13 @@ kd_status fused_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t 
 
 kd_status fused_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t T_norm, int64_t d,
                     int64_t V, const RowTerms& rt, int64_t chunk, float tau, const float* lse,
-                    const float* grad_loss, void* dH, float* dW, int accumulate, void* ws,
-                    cudaStream_t s, int num_sms, uint64_t limit_ns) {
+                    const float* grad_loss, void* dH, void* dW, int dW_dtype, int accumulate,
+                    void* ws, cudaStream_t s, int num_sms, uint64_t limit_ns) {
   if (dtype == KD_DTYPE_F32)
-    return bwd_impl<float>(h, W, T, T_norm, d, V, rt, chunk, tau, lse, grad_loss, dH, dW,
+    return bwd_impl<float>(h, W, T, T_norm, d, V, rt, chunk, tau, lse, grad_loss, dH, dW, dW_dtype,
                            accumulate, ws, s, num_sms, limit_ns);
   return bwd_impl<__nv_bfloat16>(h, W, T, T_norm, d, V, rt, chunk, tau, lse, grad_loss, dH, dW,
-                                 accumulate, ws, s, num_sms, limit_ns);
+                                 dW_dtype, accumulate, ws, s, num_sms, limit_ns);
 }
 
 cudaError_t launch_wait_probe(uint32_t* status, uint64_t limit_ns, cudaStream_t s) {

@@ -18,7 +18,9 @@ tokens, and ``policy_loss``, ``PolicyLoss``, ``preference_loss`` and
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
+import operator
 import os
 import re
 
@@ -70,7 +72,7 @@ _SIGNATURES = {
     "kd_head_logprob_fwd": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
                                      ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
     "kd_head_logprob_bwd": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
-                                     ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int,
+                                     ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
                                      _c_vp, _c_sz, _c_vp]),
     "kd_policy_loss_workspace_size": (_c_sz, [_c_i64, _c_i64]),
     "kd_policy_loss": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_i64, _c_i64, _c_f64,
@@ -219,10 +221,10 @@ def kd_head_logprob_fwd(h, W, dtype, T, d, V, targets, chunk, temperature, logp,
 
 
 def kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse, grad_logp, grad_loss,
-                        dH, dW, accumulate_dW, ws, ws_bytes, stream):
+                        dH, dW, dW_dtype, accumulate_dW, ws, ws_bytes, stream):
     return load().kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse,
-                                      grad_logp, grad_loss, dH, dW, accumulate_dW, ws, ws_bytes,
-                                      stream)
+                                      grad_logp, grad_loss, dH, dW, dW_dtype, accumulate_dW, ws,
+                                      ws_bytes, stream)
 
 
 def kd_policy_loss_workspace_size(n_seqs, n_tokens):
@@ -496,14 +498,23 @@ def _require(name: str, t, dtype, shape, device):
         raise ValueError(f"{name}: must be contiguous")
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _use_stream(device, stream):
     """Context in which a call's outputs and workspace are allocated and its
     kernels launched: the given stream, or the device's current one."""
     if stream is None:
-        return torch.cuda.device(device)
+        index = device.index
+        return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
     if stream.device != device:
         raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
     return torch.cuda.stream(stream)
+
+
+def _current_stream(device) -> int:
+    # by the device's index: looking up an unnamed current device costs more than the launch
+    return torch.cuda.current_stream(device.index).cuda_stream
 
 
 def _head_sizes(h, W, targets):
@@ -535,17 +546,18 @@ def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, 
         lse = torch.empty((T,), dtype=torch.float32, device=h.device)
         _check(kd_head_logprob_fwd(h.data_ptr(), W.data_ptr(), code, T, d, V, targets.data_ptr(),
                                    chunk, float(temperature), logp.data_ptr(), lse.data_ptr(),
-                                   ws.data_ptr(), ws.numel(), _stream()),
+                                   ws.data_ptr(), ws.numel(), _current_stream(h.device)),
                "kd_head_logprob_fwd")
     return logp, lse, ws
 
 
 def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: float = 1.0,
                       grad_loss=None, ws=None, dH=None, dW=None, accumulate_dW: bool = False,
-                      stream=None, need=(True, True)):
+                      stream=None, need=(True, True), dW_dtype=torch.float32):
     """Gradients of sum_t grad_logp[t] * logp[t] (times the device scalar
     ``grad_loss``): (dH [T, d] dtype of h, dW [V, d] f32, ws).  The logits are
-    recomputed chunk by chunk; ``accumulate_dW=True`` adds into a given dW.
+    recomputed chunk by chunk; ``accumulate_dW=True`` adds into a given dW;
+    ``dW_dtype=torch.bfloat16`` gives a bf16 dW where T <= 2 chunk.
     ``need=(dH, dW)`` leaves out a gradient that is not wanted (None in its
     place)."""
     T, d, V, code = _head_sizes(h, W, targets)
@@ -557,6 +569,8 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
             raise ValueError("grad_loss: one value is needed")
     if accumulate_dW and dW is None:
         raise ValueError("accumulate_dW: needs the dW to add to")
+    if dW_dtype is not torch.float32 and dW_dtype is not torch.bfloat16:
+        raise TypeError(f"dW_dtype: float32 or bfloat16 is needed, not {dW_dtype}")
     if not any(need):
         raise ValueError("need: at least one gradient")
     with _use_stream(h.device, stream):
@@ -571,13 +585,14 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
         if not need[1]:
             dW = None
         elif dW is None:
-            dW = torch.empty((V, d), dtype=torch.float32, device=h.device)
+            dW = torch.empty((V, d), dtype=dW_dtype, device=h.device)
         else:
-            _require("dW", dW, torch.float32, (V, d), h.device)
+            _require("dW", dW, dW_dtype, (V, d), h.device)
         _check(kd_head_logprob_bwd(h.data_ptr(), W.data_ptr(), code, T, d, V, targets.data_ptr(),
                                    chunk, float(temperature), lse.data_ptr(), grad_logp.data_ptr(),
-                                   _ptr(grad_loss), _ptr(dH), _ptr(dW), int(accumulate_dW),
-                                   ws.data_ptr(), ws.numel(), _stream()),
+                                   _ptr(grad_loss), _ptr(dH), _ptr(dW),
+                                   KD_DTYPE_BF16 if dW_dtype is torch.bfloat16 else KD_DTYPE_F32,
+                                   int(accumulate_dW), ws.data_ptr(), ws.numel(), _current_stream(h.device)),
                "kd_head_logprob_bwd")
     return dH, dW, ws
 
@@ -597,8 +612,12 @@ class HeadLogprobs(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         h, W, targets, lse = ctx.saved_tensors
+        # dW leaves the kernel in W's type where it is formed in one go, and is added up in fp32
+        # and rounded afterwards otherwise
+        direct = h.shape[0] <= 2 * ctx.chunk
         dH, dW, _ = head_logprobs_bwd(h, W, targets, lse, g.contiguous(), ctx.chunk, ctx.temperature,
-                                      need=ctx.needs_input_grad[:2])
+                                      need=ctx.needs_input_grad[:2],
+                                      dW_dtype=W.dtype if direct else torch.float32)
         return dH, None if dW is None else dW.to(W.dtype), None, None, None
 
 
@@ -627,10 +646,11 @@ def _sequences(logp, cu_seqlens, mask):
     return n_seqs, logp.numel()
 
 
-def _scratch(nbytes: int, device):
-    """Workspace of one call: (the buffer to keep, its aligned address, bytes)."""
+def _scratch(nbytes: int, like):
+    """Workspace of one call on the device of the fp32 or bf16 tensor `like`: (the
+    buffer to keep, its aligned address, bytes)."""
     n = max(int(nbytes), 1024)
-    buf = torch.empty(n + 1024, dtype=torch.uint8, device=device)
+    buf = like.new_empty((n + 1024) // 2)
     return buf, (buf.data_ptr() + 1023) & ~1023, n
 
 
@@ -664,17 +684,17 @@ def policy_loss(logp, old_logp, advantages, *, mask=None, ref_logp=None, cu_seql
         _require("ref_logp", ref_logp, torch.float32, logp.shape, dev)
     with _use_stream(dev, stream):
         if ws is None:
-            keep, at, nbytes = _scratch(kd_policy_loss_workspace_size(n_seqs, n), dev)
+            keep, at, nbytes = _scratch(kd_policy_loss_workspace_size(n_seqs, n), logp)
         else:
             at, nbytes = ws.data_ptr(), ws.numel()
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        stats = torch.empty((4,), dtype=torch.float32, device=dev)
+        loss = logp.new_empty(())
+        stats = logp.new_empty(4)
         dlogp = torch.empty_like(logp) if grad else None
         _check(kd_policy_loss(logp.data_ptr(), _ptr(old_logp), _ptr(ref_logp), advantages.data_ptr(),
                               int(per_token), _ptr(mask), _ptr(cu_seqlens), n_seqs, n, clip_low,
                               clip_high, kl_coef, REDUCTIONS[reduction],
                               0.0 if denom is None else denom, loss.data_ptr(), stats.data_ptr(),
-                              _ptr(dlogp), at, nbytes, _stream()),
+                              _ptr(dlogp), at, nbytes, _current_stream(dev)),
                "kd_policy_loss")
     return loss, stats, dlogp
 
@@ -721,17 +741,17 @@ def preference_loss(logp, *, ref_logp=None, mask=None, cu_seqlens=None, kind: st
     pairs = n_seqs // 2
     with _use_stream(dev, stream):
         if ws is None:
-            keep, at, nbytes = _scratch(kd_preference_loss_workspace_size(pairs, n), dev)
+            keep, at, nbytes = _scratch(kd_preference_loss_workspace_size(pairs, n), logp)
         else:
             at, nbytes = ws.data_ptr(), ws.numel()
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        rewards = torch.empty((n_seqs,), dtype=torch.float32, device=dev)
+        loss = logp.new_empty(())
+        rewards = logp.new_empty(n_seqs)
         dlogp = torch.empty_like(logp) if grad else None
         _check(kd_preference_loss(logp.data_ptr(), _ptr(ref_logp), _ptr(mask), _ptr(cu_seqlens), pairs, n,
                                   PREFERENCE_KINDS[kind], beta, margin, label_smoothing,
                                   int(length_normalize), pairs if pairs_total is None else pairs_total,
                                   loss.data_ptr(), rewards.data_ptr(), _ptr(dlogp), at, nbytes,
-                                  _stream()),
+                                  _current_stream(dev)),
                "kd_preference_loss")
     return loss, rewards, dlogp
 
@@ -757,24 +777,27 @@ class PreferenceLoss(torch.autograd.Function):
 # ------------------------------------------------- the gradients of the whole step
 
 _GRAD_CODES = {torch.float32: KD_DTYPE_F32, torch.bfloat16: KD_DTYPE_BF16}
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _grad_arrays(name: str, tensors):
-    """Checks a list of gradients; (count, device, addresses, sizes, type codes)."""
+    """Checks a list of gradients; (count, device, addresses, sizes, type codes).
+    A list may hold hundreds of small tensors: every pass over it is a `map`."""
     n = len(tensors)
     if n == 0:
         raise ValueError(f"{name}: at least one tensor is needed")
+    Tensor = torch.Tensor
     try:
-        codes = [_GRAD_CODES[t.dtype] for t in tensors]
-    except (KeyError, AttributeError):
+        codes = array.array("i", map(_GRAD_CODES.__getitem__, map(_dtype_of, tensors)))
+        places = set(map(Tensor.get_device, tensors))
+    except (KeyError, AttributeError, TypeError):
         raise TypeError(f"{name}: float32 or bfloat16 tensors are needed") from None
-    device = tensors[0].device
-    if {t.get_device() for t in tensors} != {device.index} or device.type != "cuda":
+    if len(places) != 1 or not tensors[0].is_cuda:
         raise ValueError(f"{name}: all tensors must be on one CUDA device")
-    if not all([t.is_contiguous() for t in tensors]):
+    if not all(map(Tensor.is_contiguous, tensors)):
         raise ValueError(f"{name}: must be contiguous")
-    return (n, device, array.array("Q", [t.data_ptr() for t in tensors]),
-            array.array("q", [t.numel() for t in tensors]), array.array("i", codes))
+    return (n, tensors[0].device, array.array("Q", map(Tensor.data_ptr, tensors)),
+            array.array("q", map(Tensor.numel, tensors)), codes)
 
 
 def grad_sumsq(grads, stream=None):
@@ -782,10 +805,10 @@ def grad_sumsq(grads, stream=None):
     grads = list(grads)
     n, dev, ptrs, sizes, codes = _grad_arrays("grads", grads)
     with _use_stream(dev, stream):
-        keep, at, nbytes = _scratch(kd_grad_clip_workspace_size(n), dev)
+        keep, at, nbytes = _scratch(kd_grad_clip_workspace_size(n), grads[0])
         out = torch.empty((), dtype=torch.float64, device=dev)
         _check(kd_grad_sumsq(ptrs.buffer_info()[0], sizes.buffer_info()[0], codes.buffer_info()[0], n,
-                             out.data_ptr(), at, nbytes, _stream()),
+                             out.data_ptr(), at, nbytes, _current_stream(dev)),
                "kd_grad_sumsq")
     return out
 
@@ -807,10 +830,10 @@ def clip_grad_norm(grads, max_norm: float, out=None, sumsq=None, stream=None):
     if sumsq is not None:
         _require("sumsq", sumsq, torch.float64, (), dev)
     with _use_stream(dev, stream):
-        keep, at, nbytes = _scratch(kd_grad_clip_workspace_size(n), dev)
+        keep, at, nbytes = _scratch(kd_grad_clip_workspace_size(n), grads[0])
         norm = torch.empty((), dtype=torch.float32, device=dev)
         _check(kd_grad_clip(ptrs.buffer_info()[0], outs.buffer_info()[0], sizes.buffer_info()[0],
                             codes.buffer_info()[0], n, max_norm, _ptr(sumsq), norm.data_ptr(), at,
-                            nbytes, _stream()),
+                            nbytes, _current_stream(dev)),
                "kd_grad_clip")
     return norm

@@ -250,8 +250,9 @@ kd_status kd_fused_kl_bwd_shard(const void* h, const void* W, int dtype,
 /* A row with this target has no token: its logp is 0 and its gradient 0. */
 #define KD_TARGET_IGNORE (-100)
 
-/* Bytes of workspace: backward == 0 for kd_head_logprob_fwd alone (a fraction
- * of what the backward needs), otherwise for both calls. */
+/* Bytes of workspace: backward == 0 for kd_head_logprob_fwd alone (16 bytes per
+ * row of max(chunk, 2048) and 256 vocabulary entries, and 20 per position),
+ * otherwise for both calls. */
 size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int dtype,
                                       int backward);
 
@@ -259,7 +260,8 @@ size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t c
  * Forward.  h, W, dtype, T, d, V, chunk, temperature as for kd_fused_kl_fwd;
  *   targets [T] int32: y_t in [0, V), or KD_TARGET_IGNORE
  * Outputs (device): logp float32 [T], lse float32 [T] (of every row; keep it
- * for the backward).  Bit-identical for every `chunk`.  A target outside [0, V)
+ * for the backward).  Bit-identical for every `chunk`, of which the forward
+ * takes several in one launch where they are below 2048 rows.  A target outside [0, V)
  * other than KD_TARGET_IGNORE is recorded as KD_ERR_BAD_INDEX; the outputs of
  * that call are then unspecified.
  */
@@ -272,7 +274,10 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
  * (not read for ignored rows), times the device scalar grad_loss (NULL for 1):
  *   dz_tv = g grad_logp_t / tau * ([v == y_t] - exp(a_tv - LSE_t))
  *   dH = dz W -> [T, d], dtype of h (overwritten);  dW (+)= dz^T h -> [V, d]
- *   float32, overwritten or (accumulate_dW != 0) added to.
+ *   of dW_dtype: KD_DTYPE_F32, overwritten or (accumulate_dW != 0) added to;
+ *   or KD_DTYPE_BF16 for bf16 operands, rounded once from the fp32 sum, where
+ *   one is formed: T <= 2 chunk and accumulate_dW == 0 (KD_ERR_UNSUPPORTED
+ *   otherwise).
  * Either of dH and dW may be NULL: that gradient is not computed (a frozen head
  * needs no dW).  dz is rounded to the operands' type, as in kd_fused_kl_bwd.  An ignored row
  * contributes 0 times its h to dW, so h must be finite in every row.
@@ -280,8 +285,8 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
 kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
                               const float* lse, const float* grad_logp, const float* grad_loss,
-                              void* dH, float* dW, int accumulate_dW, void* ws, size_t ws_bytes,
-                              void* stream);
+                              void* dH, void* dW, int dW_dtype, int accumulate_dW, void* ws,
+                              size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Objectives of post-training over the log-probabilities of a batch's      */

@@ -20,12 +20,13 @@ def lib():
 
 def _head(call, **kw):
     a = dict(h=FAKE, W=FAKE, dtype=kd.KD_DTYPE_BF16, T=256, d=256, V=4096, targets=FAKE, chunk=64, tau=1.0,
-             logp=FAKE, lse=FAKE, g=FAKE, gl=None, dH=FAKE, dW=FAKE, ws=FAKE, ws_bytes=1 << 40)
+             logp=FAKE, lse=FAKE, g=FAKE, gl=None, dH=FAKE, dW=FAKE, dWt=0, acc=0, ws=FAKE, ws_bytes=1 << 40)
     a.update(kw)
     head = (a["h"], a["W"], a["dtype"], a["T"], a["d"], a["V"], a["targets"], a["chunk"], a["tau"])
     if call == "fwd":
         return kd.kd_head_logprob_fwd(*head, a["logp"], a["lse"], a["ws"], a["ws_bytes"], None)
-    return kd.kd_head_logprob_bwd(*head, a["lse"], a["g"], a["gl"], a["dH"], a["dW"], 0, a["ws"], a["ws_bytes"], None)
+    return kd.kd_head_logprob_bwd(*head, a["lse"], a["g"], a["gl"], a["dH"], a["dW"], a["dWt"], a["acc"], a["ws"],
+                                  a["ws_bytes"], None)
 
 
 @pytest.mark.parametrize("call", ["fwd", "bwd"])
@@ -43,6 +44,10 @@ def test_head_logprob_refusals(call):
         assert _head(call, g=None) == kd.KD_ERR_INVALID_ARG
         assert _head(call, dH=None, dW=None) == kd.KD_ERR_INVALID_ARG
         assert _head(call, gl=FAKE + 2) == kd.KD_ERR_INVALID_ARG
+        # a bf16 dW: of bf16 operands, formed in one go, not added to
+        for kw in (dict(dWt=2), dict(dWt=1), dict(dWt=1, chunk=127), dict(dWt=1, chunk=256, acc=1),
+                   dict(dWt=1, chunk=256, dtype=kd.KD_DTYPE_F32)):
+            assert _head(call, **kw) == kd.KD_ERR_UNSUPPORTED, kw
 
 
 def test_head_workspace_sizes():

@@ -148,6 +148,15 @@ def test_autograd_frozen_head_and_accumulation():
     hl, Wl = h.clone().requires_grad_(), W.clone().requires_grad_()
     gh, gw = torch.autograd.grad(kd.HeadLogprobs.apply(hl, Wl, tgt, 48, 1.0), (hl, Wl), g)
     assert torch.equal(gh, dH) and torch.equal(gw, dW.to(torch.bfloat16))
+    # formed in one go, dW leaves the kernel in bf16: the rounding of the fp32 one
+    for chunk in (65, 130, 1000):
+        _, w32, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk)
+        _, w16, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk, dW_dtype=torch.bfloat16)
+        assert w16.dtype is torch.bfloat16 and torch.equal(w16, w32.to(torch.bfloat16))
+        gh, gw = torch.autograd.grad(kd.HeadLogprobs.apply(hl, Wl, tgt, chunk, 1.0), (hl, Wl), g)
+        assert torch.equal(gw, w16)
+    with pytest.raises(kd.KDError):
+        kd.head_logprobs_bwd(h, W, tgt, lse, g, 64, dW_dtype=torch.bfloat16)
     hf = h.clone().requires_grad_()
     (only,) = torch.autograd.grad(kd.HeadLogprobs.apply(hf, W, tgt, 48, 1.0), (hf,), g)
     assert torch.equal(only, dH)
