@@ -350,15 +350,26 @@ static kd_status validate_layout(const int32_t* cu, int64_t n_seqs, int64_t n_to
   q->S = static_cast<int32_t>(n_seqs);
   q->N = static_cast<int32_t>(n_tokens);
   q->L = cu ? 0 : static_cast<int32_t>(n_tokens / n_seqs);
+  if (q->L > 1) {
+    int log = 0;                                     // ceil(log2 L), at most 31
+    while ((int64_t(1) << log) < q->L) ++log;
+    q->div_mul = static_cast<uint32_t>(((uint64_t(1) << (31 + log)) + q->L - 1) / q->L);
+    q->div_shift = static_cast<uint32_t>(log - 1);
+  }
   return KD_OK;
 }
 
 static size_t up1024(size_t x) { return (x + 1023) & ~size_t(1023); }
 
+// Bytes for the counts of the mask, of each sequence or of each block's part.
+static size_t policy_counts(int64_t n_seqs) {
+  return up1024(4 * static_cast<size_t>(n_seqs > kd::OBJ_MAX_COUNTS ? n_seqs : kd::OBJ_MAX_COUNTS));
+}
+
 size_t kd_policy_loss_workspace_size(int64_t n_seqs, int64_t n_tokens) {
   if (n_seqs < 1 || n_tokens < 1 || n_seqs > kd::OBJ_MAX_TOKENS || n_tokens > kd::OBJ_MAX_TOKENS)
     return 0;
-  return kd::OBJ_HEADER + up1024(4 * static_cast<size_t>(n_seqs)) +
+  return kd::OBJ_HEADER + policy_counts(n_seqs) +
          kd::OBJ_MAX_BLOCKS * kd::OBJ_PARTIALS * sizeof(double);
 }
 
@@ -405,10 +416,8 @@ kd_status kd_policy_loss(const float* logp, const float* old_logp, const float* 
   unsigned char* w = static_cast<unsigned char*>(ws);
   a.status = reinterpret_cast<uint32_t*>(w);
   a.ticket = reinterpret_cast<uint32_t*>(w + 8);
-  a.count = reinterpret_cast<uint32_t*>(
-      w + (reduction == KD_REDUCE_SEQUENCE ? kd::OBJ_HEADER : 16));
-  a.partials = reinterpret_cast<double*>(w + kd::OBJ_HEADER +
-                                         up1024(4 * static_cast<size_t>(n_seqs)));
+  a.count = reinterpret_cast<uint32_t*>(w + kd::OBJ_HEADER);
+  a.partials = reinterpret_cast<double*>(w + kd::OBJ_HEADER + policy_counts(n_seqs));
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
   return kd::policy_loss(a, static_cast<cudaStream_t>(stream), sms);
@@ -459,14 +468,13 @@ kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uin
   a.smoothing = label_smoothing;
   a.inv_pairs = 1.0 / static_cast<double>(pairs_total);
   a.span = static_cast<int32_t>(kd::pref_span(n_tokens));
-  a.n_spans = (n_tokens + a.span - 1) / a.span;
+  a.n_spans = static_cast<int32_t>((n_tokens + a.span - 1) / a.span);
   a.loss = loss;
   a.rewards = rewards;
   a.dlogp = dlogp;
   unsigned char* w = static_cast<unsigned char*>(ws);
   const size_t S = 2 * static_cast<size_t>(n_pairs), part = sizeof(kd::SeqPart);
   a.status = reinterpret_cast<uint32_t*>(w);
-  a.ticket = reinterpret_cast<uint32_t*>(w + 8);
   w += kd::OBJ_HEADER;
   a.whole = reinterpret_cast<kd::SeqPart*>(w);
   w += up1024(S * part);

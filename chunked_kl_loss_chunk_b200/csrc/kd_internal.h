@@ -98,14 +98,16 @@ cudaError_t launch_topk_bf16(const void* logits, int64_t T, int64_t V, int K, fl
 struct SeqLayout {
   const int32_t* cu;
   int32_t S, N, L;
+  uint32_t div_mul, div_shift;      // t / L == umulhi(t, div_mul) >> div_shift, for L > 1
 };
 
 // Largest number of tokens or sequences: the kernels' token offsets, with what
 // they read ahead of one, stay below 2^31.
 constexpr int64_t OBJ_MAX_TOKENS = (int64_t(1) << 31) - 1024;
 // First region of an objective's workspace: status word at byte 0, ticket of
-// the last block at byte 8, count of unmasked tokens at byte 16.
+// the last block at byte 8.
 constexpr size_t OBJ_HEADER = 1024;
+constexpr int64_t OBJ_MAX_COUNTS = 1024;   // counts of the mask, one a block
 constexpr int64_t OBJ_MAX_BLOCKS = 2048;   // blocks that leave partial sums
 constexpr int OBJ_PARTIALS = 5;            // sums a block of the policy loss leaves
 
@@ -119,7 +121,9 @@ struct PolicyArgs {
   double log_hi64, log_lo64;
   float kl_coef, inv_denom;
   float *loss, *stats, *dlogp;
-  uint32_t *status, *ticket, *count;
+  uint32_t *status, *ticket;
+  uint32_t* count;                  // unmasked tokens of each sequence, or of each block's part
+  int32_t n_counts;                 // of the second kind
   double* partials;
 };
 
@@ -138,9 +142,9 @@ struct PrefArgs {
   int kind, normalize;
   double beta, margin, smoothing, inv_pairs;
   int32_t span;                     // tokens a warp sums, a multiple of 128
-  int64_t n_spans;
+  int32_t n_spans;
   float *loss, *rewards, *dlogp;
-  uint32_t *status, *ticket;
+  uint32_t* status;
   SeqPart *whole, *head, *tail;     // [S], [n_spans], [n_spans]
   float* coef;                      // [S] gradient of each of a sequence's tokens
   double* partials;
@@ -148,9 +152,9 @@ struct PrefArgs {
 
 kd_status preference_loss(const PrefArgs& a, cudaStream_t s, int num_sms);
 
-// Tokens a warp sums: about one span for each of the warps that fill the
-// device, but whole rows of 128.
-constexpr int64_t PREF_WARPS = 148 * 48;
+// Tokens a warp sums: one span for each of the warps that are resident at once
+// (32 an SM), in whole rows of 128.
+constexpr int64_t PREF_WARPS = 148 * 32;
 inline int64_t pref_span(int64_t n_tokens) {
   const int64_t rows = (n_tokens + 127) / 128;
   return 128 * ((rows + PREF_WARPS - 1) / PREF_WARPS);

@@ -26,10 +26,16 @@ __device__ __forceinline__ int32_t seq_begin(const SeqLayout& q, int32_t b) {
   return min(max(__ldg(q.cu + b), 0), q.N);
 }
 
+// t / L for 0 <= t < 2^31 by a multiplication (Granlund and Montgomery, "Division
+// by invariant integers using multiplication", 1994): the host gives ceil(2^p / L).
+__device__ __forceinline__ int32_t row_of(const SeqLayout& q, int32_t t) {
+  return q.L == 1 ? t : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(t), q.div_mul) >> q.div_shift);
+}
+
 // Sequence of token t: the last b with begin(b) <= t, so that empty sequences
 // are passed over.  -1 before the first sequence, S behind the last.
 __device__ __forceinline__ int32_t seq_of(const SeqLayout& q, int32_t t) {
-  if (!q.cu) return static_cast<int32_t>(static_cast<uint32_t>(t) / static_cast<uint32_t>(q.L));
+  if (!q.cu) return row_of(q, t);
   int32_t lo = -1, hi = q.S;
   while (lo < hi) {
     const int32_t mid = lo + (hi - lo + 1) / 2;
@@ -38,15 +44,36 @@ __device__ __forceinline__ int32_t seq_of(const SeqLayout& q, int32_t t) {
   return lo;
 }
 
+// The same for one token by a whole warp: 32 probes a step, so that a batch of
+// 1000 sequences takes two dependent loads and not ten.
+__device__ __forceinline__ int32_t seq_of_warp(const SeqLayout& q, int32_t t, int lane) {
+  if (!q.cu) return row_of(q, t);
+  int32_t lo = -1, n = q.S + 2;            // the answer is one of lo .. lo + n - 1
+  while (n > 1) {
+    const int32_t step = (n + 31) / 32;
+    const int64_t at = static_cast<int64_t>(lo) + static_cast<int64_t>(lane + 1) * step;
+    const bool before = at <= q.S && __ldg(q.cu + at) <= t;
+    // an ascending cu sets the lowest lanes; of any other, the run of them is taken
+    const int k = __ffs(~__ballot_sync(0xffffffffu, before)) - 1;
+    const int32_t skip = (k < 0 ? 32 : k) * step;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
 // A token's sequence and where that sequence ends.
 struct Cursor {
   int32_t b, e;
 };
+__device__ __forceinline__ Cursor cursor_of(const SeqLayout& q, int32_t b) {
+  return Cursor{b, b >= q.S ? INT_MAX : seq_begin(q, b + 1)};   // b == -1: ends where the first begins
+}
 __device__ __forceinline__ Cursor cursor_at(const SeqLayout& q, int32_t t) {
-  Cursor c;
-  c.b = seq_of(q, t);
-  c.e = c.b >= q.S ? INT_MAX : seq_begin(q, c.b + 1);   // b == -1: the first sequence's begin
-  return c;
+  return cursor_of(q, seq_of(q, t));
+}
+__device__ __forceinline__ Cursor cursor_at_warp(const SeqLayout& q, int32_t t, int lane) {
+  return cursor_of(q, seq_of_warp(q, t, lane));
 }
 
 // Records KD_ERR_BAD_INDEX unless 0 <= cu[0] <= cu[1] <= ... <= cu[S] <= N.
@@ -60,32 +87,71 @@ __device__ __forceinline__ void check_layout(const SeqLayout& q, uint32_t* statu
   }
 }
 
-// Four consecutive tokens from t (a multiple of 4): values, or `fill` beyond N.
-__device__ __forceinline__ void load4(const float* p, int32_t t, int32_t N, float fill,
-                                      float (&v)[4]) {
-  if (t + 4 <= N) {
-    const float4 q = __ldg(reinterpret_cast<const float4*>(p + t));
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = t + j < N ? __ldg(p + t + j) : fill;
-  }
-}
+// ----------------------------------------------------------------------------
+// Rows of 128 tokens, four a lane, copied asynchronously into shared memory some
+// rows ahead of their use.  A lane copies and reads its own tokens alone, so the
+// copies need no barrier.  With the loads of the next row held in registers
+// instead, the sums of the preference loss over 4.2M tokens took 15 us, waiting for
+// memory at 28 warps an SM; they take 10 us.  The mask is loaded one row further
+// ahead, into registers, and a row in which no token counts (a prompt, padding) is
+// not copied at all.
+// ----------------------------------------------------------------------------
+template <int ARRAYS, int DEPTH>
+struct RowQueue {
+  static constexpr int ROW = ARRAYS * 512;            // bytes of a row
+  static constexpr int WARP = DEPTH * ROW;
+  unsigned char* at;                                  // this lane's places
 
-// Bit j: token t + j lies in the batch and its mask byte is not 0.
-__device__ __forceinline__ uint32_t load_mask4(const uint8_t* p, int32_t t, int32_t N) {
-  if (!p) return t + 4 <= N ? 0xFu : (t < N ? (1u << (N - t)) - 1u : 0u);
-  uint32_t m = 0;
-  if (t + 4 <= N) {
-    const uchar4 q = __ldg(reinterpret_cast<const uchar4*>(p + t));
-    m = (q.x ? 1u : 0u) | (q.y ? 2u : 0u) | (q.z ? 4u : 0u) | (q.w ? 8u : 0u);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (t + j < N && __ldg(p + t + j)) m |= 1u << j;
+  // The four values from p, of which the first `left` lie in the array; 0 in the places of
+  // the others.
+  __device__ __forceinline__ void copy(int slot, int k, const float* p, int left) const {
+    const uint32_t to = smem_u32(at + slot * ROW + k * 512);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p),
+                 "r"(left < 4 ? 4 * left : 16)
+                 : "memory");
   }
+  __device__ __forceinline__ void commit() const {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // No copy is under way (a walk may end before it has used all that it asked for).
+  __device__ __forceinline__ void drain() const {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  // The oldest row of DEPTH committed ones has arrived.
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+  }
+  __device__ __forceinline__ void read(int slot, int k, float (&v)[4]) const {
+    const float4 q = *reinterpret_cast<const float4*>(at + slot * ROW + k * 512);
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+  }
+};
+
+// Mask bytes with those outside [first, last) cleared.
+__device__ __forceinline__ uint32_t inside(uint32_t m, int32_t t, int32_t first, int32_t last) {
+  if (t >= first && t + 4 <= last) return m;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (t + j < first || t + j >= last) m &= ~(0xFFu << (8 * j));
   return m;
 }
+__device__ __forceinline__ bool mask_byte(uint32_t m, int j) { return m & (0xFFu << (8 * j)); }
+// 0x80 in each byte that is not 0.
+__device__ __forceinline__ uint32_t byte_flags(uint32_t w) {
+  return (((w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w) & 0x80808080u;
+}
+
+// Mask bytes of four tokens, straight from memory.
+__device__ __forceinline__ uint32_t load_mask4(const uint8_t* p, int32_t t, int32_t N) {
+  if (t >= N) return 0u;
+  if (!p) return t + 4 <= N ? 0x01010101u : 0x01010101u >> (8 * (4 - (N - t)));
+  if (t + 4 <= N) return __ldg(reinterpret_cast<const uint32_t*>(p + t));
+  uint32_t m = 0;
+  for (int j = 0; j < N - t; ++j) m |= static_cast<uint32_t>(__ldg(p + t + j)) << (8 * j);
+  return m;
+}
+
+__device__ __forceinline__ int32_t rows_of(const SeqLayout& q) { return (q.N + 127) / 128; }
 
 __device__ __forceinline__ void store4(float* p, int32_t t, int32_t N, const float (&v)[4]) {
   if (t + 4 <= N) {
@@ -117,61 +183,128 @@ __device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t* sm_flag) 
 //   clipped: A > 0 and r > 1 + hi, or A < 0 and r < 1 - lo
 // weighted by 1 / sum m, 1 / (S n_b) or 1 / denom.  The weight needs the counts
 // of the mask first: a pass over the mask alone (1 byte a token) runs before
-// the main one.  Integer atomics add the counts, whose order does not matter.
+// the main one.
 // ----------------------------------------------------------------------------
 constexpr int OBJ_THREADS = 256;
-constexpr int POLICY_STATS = 5;   // loss, tokens, ratios, clipped, KL
+constexpr int POLICY_STATS = 5;   // sums: loss, tokens, r, clipped, KL
+constexpr int PREF_BLOCKS_PER_SM = 4;
+constexpr int POLICY_BLOCKS_PER_SM = 3;
 
-// e^q - 1 - q without the cancellation of small q: q^2 times the Taylor series of
-// (e^q - 1 - q) / q^2, whose first left-out term is below 2^-24 of it for |q| < 1/2.
-__device__ __forceinline__ float exp_minus_linear(float q) {
-  if (fabsf(q) < 0.5f) {
-    float s = 1.f / 362880.f;
-    s = fmaf(s, q, 1.f / 40320.f);
-    s = fmaf(s, q, 1.f / 5040.f);
-    s = fmaf(s, q, 1.f / 720.f);
-    s = fmaf(s, q, 1.f / 120.f);
-    s = fmaf(s, q, 1.f / 24.f);
-    s = fmaf(s, q, 1.f / 6.f);
-    s = fmaf(s, q, 0.5f);
-    return q * q * s;
-  }
-  return expf(q) - 1.f - q;
+// Two fp32 values that one instruction works on (fma.rn.f32x2 and its like): the
+// main pass is bound by the instructions it issues once its rows arrive in time.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void f2_get(const F2& a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(const F2& a, const F2& b, const F2& c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(const F2& a, const F2& b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(const F2& a, const F2& b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 
-// Mask counts, into count[0] (all sequences) or count[b].
-__device__ __forceinline__ void policy_count(const PolicyArgs& a, int32_t warp, int32_t n_warps,
-                                             int lane) {
-  const SeqLayout& q = a.seq;
-  const bool per_seq = a.reduction == KD_REDUCE_SEQUENCE;
-  const int32_t first = seq_begin(q, 0), last = seq_begin(q, q.S);
+// e^x as 2^(x log2 e), with the hardware's 2^y (2^-22 of the value): the error of
+// the product adds |x| 2^-24, as much as the rounding of x itself.
+__device__ __forceinline__ F2 exp2v(const F2& x) {
+  float lo, hi;
+  f2_get(mul2(x, f2(1.44269504088896341f)), lo, hi);
+  return f2(ex2_approx(lo), ex2_approx(hi));
+}
+
+// k = e^q - 1 - q without the cancellation of small q: q^2 times the Taylor series
+// of (e^q - 1 - q) / q^2, whose first left-out term is below 2^-20 of it for
+// |q| < 1/2.  Both forms are computed: a warp's tokens would take both branches as
+// a rule.
+__device__ __forceinline__ F2 exp_minus_linear(const F2& q) {
+  F2 s = f2(1.f / 5040.f);
+  s = fma2(s, q, f2(1.f / 720.f));
+  s = fma2(s, q, f2(1.f / 120.f));
+  s = fma2(s, q, f2(1.f / 24.f));
+  s = fma2(s, q, f2(1.f / 6.f));
+  s = fma2(s, q, f2(0.5f));
+  s = mul2(mul2(q, q), s);
+  const F2 far = fma2(q, f2(-1.f), add2(exp2v(q), f2(-1.f)));
+  float q0, q1, s0, s1, f0, f1;
+  f2_get(q, q0, q1);
+  f2_get(s, s0, s1);
+  f2_get(far, f0, f1);
+  return f2(fabsf(q0) < 0.5f ? s0 : f0, fabsf(q1) < 0.5f ? s1 : f1);
+}
+
+// Number of the 16 tokens from t0 that the mask keeps, as bits.
+__device__ __forceinline__ uint32_t mask_bits16(const PolicyArgs& a, int32_t t0) {
+  uint32_t m = 0;
+  if (t0 + 16 <= a.seq.N) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.mask + t0));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // the four bytes' flags, gathered into four bits
+      m |= ((byte_flags(w[i]) >> 7) * 0x10204080u >> 28) << (4 * i);
+    }
+  } else {
+    for (int j = 0; j < 16; ++j)
+      if (t0 + j < a.seq.N && __ldg(a.mask + t0 + j)) m |= 1u << j;
+  }
+  return m;
+}
+
+// Unmasked tokens of all sequences among this thread's 16-token pieces.
+__device__ __forceinline__ uint32_t policy_count_all(const PolicyArgs& a, int64_t thread,
+                                                     int64_t n_threads) {
+  const int32_t first = seq_begin(a.seq, 0), last = seq_begin(a.seq, a.seq.S);
   uint32_t total = 0;
+  for (int64_t i = thread * 16; i < a.seq.N; i += n_threads * 16) {
+    const int32_t t0 = static_cast<int32_t>(i);
+    uint32_t m = mask_bits16(a, t0);
+    if (t0 < first || t0 + 16 > last)
+      for (int j = 0; j < 16; ++j)
+        if (t0 + j < first || t0 + j >= last) m &= ~(1u << j);
+    total += __popc(m);
+  }
+  return total;
+}
+
+// Sum of a count over the block, in every thread.
+__device__ __forceinline__ uint32_t block_count(uint32_t n, uint32_t* sm) {
+  n = __reduce_add_sync(0xffffffffu, n);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = n;
+  __syncthreads();
+  n = 0;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) n += sm[i];
+  __syncthreads();
+  return n;
+}
+
+// Unmasked tokens of each sequence, added to count[b] (zero before).  A warp takes
+// 512 tokens at a time; integer atomics, whose order does not matter.
+__device__ __forceinline__ void policy_count_each(const PolicyArgs& a, int32_t warp,
+                                                  int32_t n_warps, int lane) {
+  const SeqLayout& q = a.seq;
   for (int64_t row = static_cast<int64_t>(warp) * 512; row < q.N;
        row += static_cast<int64_t>(n_warps) * 512) {
     const int32_t t0 = static_cast<int32_t>(row) + lane * 16;    // row + 512 <= N + 511 < 2^31
-    uint32_t m = 0;
-    if (t0 + 16 <= q.N) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.mask + t0));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if ((w[i] >> (8 * j)) & 0xFFu) m |= 1u << (4 * i + j);
-    } else {
-      for (int j = 0; j < 16; ++j)
-        if (t0 + j < q.N && __ldg(a.mask + t0 + j)) m |= 1u << j;
-    }
-    if (!per_seq) {
-      if (q.cu && (t0 < first || t0 + 16 > last)) {
-        for (int j = 0; j < 16; ++j)
-          if (t0 + j < first || t0 + j >= last) m &= ~(1u << j);
-      }
-      total += __popc(m);
-      continue;
-    }
-    Cursor c{q.S, INT_MAX};
-    if (t0 < q.N) c = cursor_at(q, t0);
+    const uint32_t m = mask_bits16(a, t0);
+    // the row's sequence; a lane looks up its own where the row's ends before it
+    Cursor c = cursor_at_warp(q, static_cast<int32_t>(row), lane);
+    if (t0 >= c.e && t0 < q.N) c = cursor_at(q, t0);
     int same;
     __match_all_sync(0xffffffffu, c.e >= t0 + 16 ? c.b : -2 - lane, &same);
     if (same) {
@@ -189,95 +322,205 @@ __device__ __forceinline__ void policy_count(const PolicyArgs& a, int32_t warp, 
       }
     }
   }
-  if (!per_seq) {
-    total = __reduce_add_sync(0xffffffffu, total);
-    if (lane == 0 && total) atomicAdd(a.count, total);
-  }
 }
 
-// The main pass over this thread's groups of four tokens; sums into v.
-__device__ __forceinline__ void policy_tokens(const PolicyArgs& a, int64_t thread,
-                                              int64_t n_threads, double (&v)[POLICY_STATS]) {
+// What a row's tokens share where one sequence holds them all: as loaded, for the
+// row after the one at hand.
+struct PolicyLook {
+  Cursor c;
+  float adv;
+  int32_t n;
+};
+__device__ __forceinline__ void policy_look(const PolicyArgs& a, const Cursor& c, PolicyLook& l) {
+  const int32_t b = min(max(c.b, 0), a.seq.S - 1);
+  l.c = c;
+  if (!a.adv_per_token) l.adv = __ldg(a.adv + b);
+  if (a.reduction == KD_REDUCE_SEQUENCE)
+    l.n = a.mask ? static_cast<int32_t>(__ldcg(a.count + b)) : c.e - seq_begin(a.seq, b);
+}
+
+constexpr int POLICY_DEPTH = 2;
+using PolicyQueue = RowQueue<4, POLICY_DEPTH>;
+
+// Mask of a lane's tokens of a row: 0 beyond the batch and outside every sequence.
+__device__ __forceinline__ uint32_t policy_mask(const PolicyArgs& a, int32_t row, int32_t n_rows,
+                                                int32_t first, int32_t last, int lane) {
+  if (row >= n_rows) return 0u;
+  const int32_t t = row * 128 + 4 * lane;
+  const uint32_t m = load_mask4(a.mask, t, a.seq.N);
+  return a.seq.cu ? inside(m, t, first, last) : m;
+}
+
+// Starts the copies of a row with mask m, if any of its tokens counts.
+template <bool OLD, bool REF>
+__device__ __forceinline__ void policy_fetch(const PolicyArgs& a, const PolicyQueue& rows, int slot,
+                                             int32_t row, uint32_t m, int lane) {
+  if (__any_sync(0xffffffffu, m != 0)) {
+    const int32_t t = row * 128 + 4 * lane, left = a.seq.N - t;
+    if (left > 0) {
+      rows.copy(slot, 0, a.logp + t, left);
+      if (OLD) rows.copy(slot, 1, a.old_logp + t, left);
+      if (REF) rows.copy(slot, 2, a.ref_logp + t, left);
+      if (a.adv_per_token) rows.copy(slot, 3, a.adv + t, left);
+    }
+  }
+  rows.commit();
+}
+
+// The masks of a warp's next rows, and the copies of those but the last under way.
+struct PolicyAhead {
+  uint32_t m[POLICY_DEPTH + 1];
+};
+template <bool OLD, bool REF>
+__device__ __forceinline__ void policy_start(const PolicyArgs& a, const PolicyQueue& rows,
+                                             int32_t row, int32_t n_warps, PolicyAhead& ahead,
+                                             int lane) {
+  const int32_t n_rows = rows_of(a.seq), first = seq_begin(a.seq, 0);
+  const int32_t last = seq_begin(a.seq, a.seq.S);
+#pragma unroll
+  for (int k = 0; k <= POLICY_DEPTH; ++k)
+    ahead.m[k] = policy_mask(a, row + k * n_warps, n_rows, first, last, lane);
+#pragma unroll
+  for (int k = 0; k < POLICY_DEPTH; ++k)
+    policy_fetch<OLD, REF>(a, rows, k, row + k * n_warps, ahead.m[k], lane);
+}
+
+__device__ __forceinline__ void policy_add(double (&v)[POLICY_STATS], const F2& loss,
+                                           const F2& ratio, const F2& kl) {
+  float x, y;
+  f2_get(loss, x, y);
+  v[0] += x + y;
+  f2_get(ratio, x, y);
+  v[2] += x + y;
+  f2_get(kl, x, y);
+  v[4] += x + y;
+}
+
+// The main pass.  A warp takes rows of 128 tokens, `row` and every n_warps-th
+// after it, the first of them under way (policy_start).  Sums go to v:
+// fp32 over at most 16 rows of a lane's tokens, then fp64 (a conversion to fp64
+// takes the time of 16 fp32 operations).  n_all: the tokens that count, for
+// KD_REDUCE_TOKEN.
+template <bool OLD, bool REF>
+__device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQueue& queue,
+                                              int32_t row, int32_t n_warps, uint32_t n_all,
+                                              PolicyAhead& ahead, int lane,
+                                              double (&v)[POLICY_STATS]) {
   const SeqLayout& q = a.seq;
   const bool per_seq = a.reduction == KD_REDUCE_SEQUENCE;
-  const int32_t first = seq_begin(q, 0), last = seq_begin(q, q.S);
+  const bool need_seq = per_seq || !a.adv_per_token;
+  const int32_t first = seq_begin(q, 0), last = seq_begin(q, q.S), n_rows = rows_of(q);
   float w = a.inv_denom;
   if (a.reduction == KD_REDUCE_TOKEN) {
-    const uint32_t n = a.mask ? __ldcg(a.count) : static_cast<uint32_t>(max(last - first, 0));
+    const uint32_t n = a.mask ? n_all : static_cast<uint32_t>(max(last - first, 0));
     w = n ? 1.f / static_cast<float>(n) : 0.f;
   }
-  const bool need_seq = per_seq || !a.adv_per_token;
+  const float seqs = static_cast<float>(q.S);
   uint32_t n_tok = 0, n_clip = 0;
-  const int64_t groups = (static_cast<int64_t>(q.N) + 3) / 4;
-  for (int64_t g = thread; g < groups; g += n_threads) {
-    const int32_t t0 = static_cast<int32_t>(4 * g);
-    float lp[4], od[4], rf[4], av[4], out[4];
-    uint32_t m = load_mask4(a.mask, t0, q.N);
-    load4(a.logp, t0, q.N, 0.f, lp);
-    if (a.old_logp) load4(a.old_logp, t0, q.N, 0.f, od);
-    if (a.ref_logp) load4(a.ref_logp, t0, q.N, 0.f, rf);
-    if (a.adv_per_token) load4(a.adv, t0, q.N, 0.f, av);
-    if (q.cu && (t0 < first || t0 + 4 > last)) {
+  F2 s_loss = f2(0.f), s_ratio = f2(0.f), s_kl = f2(0.f);
+  uint32_t n_seen = 0;
+  int held = 0;
+  for (int slot = 0; row < n_rows; row += n_warps, slot = slot + 1 == POLICY_DEPTH ? 0 : slot + 1) {
+    const int32_t t0 = row * 128 + 4 * lane;
+    const uint32_t m = ahead.m[0];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (t0 + j < first || t0 + j >= last) m &= ~(1u << j);
-    }
-    Cursor c{-1, INT_MIN};
-    float adv = 0.f, s_loss = 0.f, s_ratio = 0.f, s_kl = 0.f;
+    for (int k = 0; k < POLICY_DEPTH; ++k) ahead.m[k] = ahead.m[k + 1];
+    ahead.m[POLICY_DEPTH] =
+        policy_mask(a, row + (POLICY_DEPTH + 1) * n_warps, n_rows, first, last, lane);
+    queue.wait();
+    float out[4] = {0.f, 0.f, 0.f, 0.f};
+    if (__any_sync(0xffffffffu, m != 0)) {
+      PolicyLook look{{0, INT_MAX}, 0.f, 1};
+      if (need_seq) policy_look(a, cursor_at_warp(q, row * 128, lane), look);
+      float lp[4], od[4], rf[4], at[4], wt[4];
+      queue.read(slot, 0, lp);
+      if (OLD) queue.read(slot, 1, od);
+      if (REF) queue.read(slot, 2, rf);
+      if (a.adv_per_token) queue.read(slot, 3, at);
+      if (per_seq) w = 1.f / (seqs * static_cast<float>(max(look.n, 1)));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      out[j] = 0.f;
-      if (!((m >> j) & 1u)) continue;       // values of masked tokens are never used
-      if (need_seq && t0 + j >= c.e) {
-        c = cursor_at(q, t0 + j);
-        const int32_t b = min(max(c.b, 0), q.S - 1);
-        if (!a.adv_per_token) adv = __ldg(a.adv + b);
-        if (per_seq) {
-          const uint32_t n = a.mask ? __ldcg(a.count + b)
-                                    : static_cast<uint32_t>(max(c.e - seq_begin(q, b), 1));
-          w = 1.f / (static_cast<float>(q.S) * static_cast<float>(n));
+      for (int j = 0; j < 4; ++j) {
+        wt[j] = w;
+        if (!a.adv_per_token) at[j] = look.adv;
+      }
+      if (need_seq && look.c.e < row * 128 + 128) {     // a sequence ends in the row
+        PolicyLook l = look;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (t0 + j >= l.c.e && t0 + j < q.N) policy_look(a, cursor_at(q, t0 + j), l);
+          if (!a.adv_per_token) at[j] = l.adv;
+          // at least 1: the weight of a token that does not count is multiplied, too
+          if (per_seq) wt[j] = 1.f / (seqs * static_cast<float>(max(l.n, 1)));
         }
       }
-      const float A = a.adv_per_token ? av[j] : adv;
-      float d = 0.f, r = 1.f;
-      bool clip = false;
-      if (a.old_logp) {
-        d = lp[j] - od[j];
-        r = expf(d);
-      }
-      // r against the border in the logarithm.  d is the rounded difference, and rounding
-      // keeps order: only d equal to the rounded border needs the exact difference.
-      if (A > 0.f) {
-        clip = d > a.log_hi || (d == a.log_hi && (a.old_logp ? static_cast<double>(lp[j]) - od[j]
-                                                             : 0.0) > a.log_hi64);
-      } else if (A < 0.f) {
-        clip = d < a.log_lo || (d == a.log_lo && (a.old_logp ? static_cast<double>(lp[j]) - od[j]
-                                                             : 0.0) < a.log_lo64);
-      }
-      const float Ar = A * r;
-      float term = clip ? -A * (A > 0.f ? a.bound_hi : a.bound_lo) : -Ar;
-      float grad = clip ? 0.f : -Ar;
-      if (a.ref_logp) {
-        const float x = rf[j] - lp[j];
-        const float k = exp_minus_linear(x);
-        s_kl += k;
-        if (a.kl_coef != 0.f) {
-          term = fmaf(a.kl_coef, k, term);
-          grad = fmaf(-a.kl_coef, k + x, grad);      // 1 - e^x = -(k + x)
+      // What a token that does not count holds is replaced before it is used: with its A, d and
+      // x at 0, every term below is 0 and the ratio 1.
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const bool on0 = mask_byte(m, j), on1 = mask_byte(m, j + 1);
+        const float A0 = on0 ? at[j] : 0.f, A1 = on1 ? at[j + 1] : 0.f;
+        const F2 A = f2(A0, A1), nlp = mul2(f2(lp[j], lp[j + 1]), f2(-1.f));
+        float d0 = 0.f, d1 = 0.f;
+        F2 ratio = f2(1.f);
+        if (OLD) {
+          f2_get(add2(f2(od[j], od[j + 1]), nlp), d0, d1);      // -d
+          d0 = on0 ? -d0 : 0.f;
+          d1 = on1 ? -d1 : 0.f;
+          ratio = exp2v(f2(d0, d1));
+          s_ratio = add2(s_ratio, ratio);
         }
+        // r against the border in the logarithm.  d is the rounded difference, and rounding
+        // keeps order: only d equal to the rounded border needs the exact difference.
+        // (For A < 0 both sides are negated.)
+        const bool up0 = A0 > 0.f, up1 = A1 > 0.f;
+        const float border0 = up0 ? a.log_hi : -a.log_lo, border1 = up1 ? a.log_hi : -a.log_lo;
+        const float e0 = up0 ? d0 : -d0, e1 = up1 ? d1 : -d1;
+        bool clip0 = e0 > border0 && A0 != 0.f, clip1 = e1 > border1 && A1 != 0.f;
+        if (e0 == border0 || e1 == border1) {
+          const double x0 = OLD && on0 ? static_cast<double>(lp[j]) - od[j] : 0.0;
+          const double x1 = OLD && on1 ? static_cast<double>(lp[j + 1]) - od[j + 1] : 0.0;
+          clip0 = A0 != 0.f && (up0 ? x0 > a.log_hi64 : x0 < a.log_lo64);
+          clip1 = A1 != 0.f && (up1 ? x1 > a.log_hi64 : x1 < a.log_lo64);
+        }
+        float r0, r1, t0_, t1_;
+        f2_get(ratio, r0, r1);
+        r0 = clip0 ? (up0 ? a.bound_hi : a.bound_lo) : r0;
+        r1 = clip1 ? (up1 ? a.bound_hi : a.bound_lo) : r1;
+        F2 term = mul2(A, f2(r0, r1));
+        f2_get(term, t0_, t1_);
+        F2 grad = f2(clip0 ? 0.f : t0_, clip1 ? 0.f : t1_);
+        if (REF) {
+          float x0, x1;
+          f2_get(add2(f2(rf[j], rf[j + 1]), nlp), x0, x1);
+          const F2 x = f2(on0 ? x0 : 0.f, on1 ? x1 : 0.f);
+          const F2 k = exp_minus_linear(x);
+          s_kl = add2(s_kl, k);
+          if (a.kl_coef != 0.f) {                      // 0 times an infinite k stays out
+            term = fma2(f2(-a.kl_coef), k, term);
+            grad = fma2(f2(a.kl_coef), add2(k, x), grad);       // 1 - e^x = -(k + x)
+          }
+        }
+        const F2 nw = f2(-wt[j], -wt[j + 1]);
+        s_loss = fma2(nw, term, s_loss);
+        n_clip += (clip0 ? 1u : 0u) + (clip1 ? 1u : 0u);
+        f2_get(mul2(nw, grad), out[j], out[j + 1]);
       }
-      s_loss = fmaf(w, term, s_loss);
-      s_ratio += r;
-      ++n_tok;
-      n_clip += clip ? 1u : 0u;
-      out[j] = w * grad;
+      n_tok += __popc(byte_flags(m));
+      n_seen += 4;
+      if (++held == 16) {
+        policy_add(v, s_loss, s_ratio, s_kl);
+        s_loss = s_ratio = s_kl = f2(0.f);
+        held = 0;
+      }
     }
-    v[0] += s_loss;
-    v[2] += s_ratio;
-    v[4] += s_kl;
-    if (a.dlogp) store4(a.dlogp, t0, q.N, out);
+    if (a.dlogp && t0 < q.N) store4(a.dlogp, t0, q.N, out);
+    policy_fetch<OLD, REF>(a, queue, slot, row + POLICY_DEPTH * n_warps, ahead.m[POLICY_DEPTH - 1],
+                           lane);
   }
+  policy_add(v, s_loss, s_ratio, s_kl);
   v[1] = n_tok;
+  if (OLD) v[2] -= n_seen - n_tok;           // the ratios of 1 of tokens that do not count
+  else v[2] = n_tok;
   v[3] = n_clip;
 }
 
@@ -290,20 +533,48 @@ __device__ __forceinline__ void policy_write(const PolicyArgs& a, const double (
   a.stats[3] = static_cast<float>(v[4] / n);
 }
 
-__global__ void __launch_bounds__(OBJ_THREADS) policy_count_kernel(const PolicyArgs a) {
+// KD_REDUCE_TOKEN: a count for each block, which the main kernel adds.
+__global__ void __launch_bounds__(OBJ_THREADS) policy_count_all_kernel(const PolicyArgs a) {
+  __shared__ uint32_t sm[OBJ_THREADS / 32];
   griddep_launch_dependents();
-  policy_count(a, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, (gridDim.x * blockDim.x) >> 5,
-               threadIdx.x & 31);
+  const uint32_t n =
+      block_count(policy_count_all(a, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+                                   static_cast<int64_t>(gridDim.x) * blockDim.x),
+                  sm);
+  if (threadIdx.x == 0) {
+    a.count[blockIdx.x] = n;
+    if (blockIdx.x == 0) *a.status = *a.ticket = 0u;
+  }
 }
 
-__global__ void __launch_bounds__(OBJ_THREADS) policy_main_kernel(const PolicyArgs a) {
-  __shared__ double sm[32 * POLICY_STATS];
-  __shared__ uint32_t flag;
-  griddep_wait();                            // the counts
+__global__ void __launch_bounds__(OBJ_THREADS) policy_count_each_kernel(const PolicyArgs a) {
+  griddep_launch_dependents();
+  policy_count_each(a, (blockIdx.x * blockDim.x + threadIdx.x) >> 5,
+                    (gridDim.x * blockDim.x) >> 5, threadIdx.x & 31);
+}
+
+template <bool OLD, bool REF>
+__global__ void __launch_bounds__(OBJ_THREADS, POLICY_BLOCKS_PER_SM)
+policy_main_kernel(const PolicyArgs a) {
+  __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PolicyQueue::WARP];
+  __shared__ double sm[OBJ_THREADS / 32 * POLICY_STATS];
+  __shared__ uint32_t flag, counts[OBJ_THREADS / 32];
+  const int lane = threadIdx.x & 31;
+  const int32_t row = (blockIdx.x * OBJ_THREADS + threadIdx.x) >> 5;
+  const int32_t n_warps = (gridDim.x * OBJ_THREADS) >> 5;
+  const PolicyQueue queue{rows + (threadIdx.x >> 5) * PolicyQueue::WARP + 16 * lane};
+  PolicyAhead ahead;
+  // the first rows do not wait for the counts
+  policy_start<OLD, REF>(a, queue, row, n_warps, ahead, lane);
+  griddep_wait();
+  uint32_t n_all = 0;
+  if (a.n_counts) {
+    for (int i = threadIdx.x; i < a.n_counts; i += OBJ_THREADS) n_all += __ldcg(a.count + i);
+    n_all = block_count(n_all, counts);
+  }
   check_layout(a.seq, a.status);
   double v[POLICY_STATS] = {};
-  policy_tokens(a, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
-                static_cast<int64_t>(gridDim.x) * blockDim.x, v);
+  policy_tokens<OLD, REF>(a, queue, row, n_warps, n_all, ahead, lane, v);
   block_sum(v, sm);
   if (threadIdx.x == 0)
 #pragma unroll
@@ -320,19 +591,29 @@ __global__ void __launch_bounds__(OBJ_THREADS) policy_main_kernel(const PolicyAr
 
 // The whole loss in one block, for batches where launches cost more than the
 // tokens: the counts, then the tokens.
-__global__ void __launch_bounds__(1024) policy_one_kernel(const PolicyArgs a) {
-  __shared__ double sm[32 * POLICY_STATS];
+template <bool OLD, bool REF>
+__global__ void __launch_bounds__(OBJ_THREADS) policy_one_kernel(const PolicyArgs a) {
+  __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PolicyQueue::WARP];
+  __shared__ double sm[OBJ_THREADS / 32 * POLICY_STATS];
+  __shared__ uint32_t counts[OBJ_THREADS / 32];
+  constexpr int NW = OBJ_THREADS / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const PolicyQueue queue{rows + warp * PolicyQueue::WARP + 16 * lane};
+  PolicyAhead ahead;
+  policy_start<OLD, REF>(a, queue, warp, NW, ahead, lane);
   if (threadIdx.x == 0) *a.status = 0u;
-  if (a.mask && a.reduction != KD_REDUCE_FIXED) {
-    const int32_t n = a.reduction == KD_REDUCE_SEQUENCE ? a.seq.S : 1;
-    for (int32_t b = threadIdx.x; b < n; b += blockDim.x) a.count[b] = 0u;
+  uint32_t n_all = 0;
+  if (a.mask && a.reduction == KD_REDUCE_SEQUENCE) {
+    for (int32_t b = threadIdx.x; b < a.seq.S; b += OBJ_THREADS) a.count[b] = 0u;
     __syncthreads();
-    policy_count(a, threadIdx.x >> 5, blockDim.x >> 5, threadIdx.x & 31);
+    policy_count_each(a, warp, NW, lane);
+  } else if (a.mask && a.reduction == KD_REDUCE_TOKEN) {
+    n_all = block_count(policy_count_all(a, threadIdx.x, OBJ_THREADS), counts);
   }
   __syncthreads();
   check_layout(a.seq, a.status);
   double v[POLICY_STATS] = {};
-  policy_tokens(a, threadIdx.x, blockDim.x, v);
+  policy_tokens<OLD, REF>(a, queue, warp, NW, n_all, ahead, lane, v);
   block_sum(v, sm);
   if (threadIdx.x == 0) policy_write(a, v);
 }
@@ -359,32 +640,72 @@ __device__ __forceinline__ void flush_part(SeqPart* to, double sum, uint32_t n, 
   if (lane == 0) *to = SeqPart{sum, static_cast<double>(n)};
 }
 
-__device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t span_i, int lane) {
+// The sequence of token t, where the one before it (c) ends: the next, unless
+// that is empty.
+__device__ __forceinline__ Cursor next_cursor(const SeqLayout& q, const Cursor& c, int32_t t,
+                                              int lane) {
+  if (c.b + 1 < q.S) {
+    const int32_t e = seq_begin(q, c.b + 2);
+    if (e > t) return Cursor{c.b + 1, e};
+  }
+  return cursor_at_warp(q, t, lane);
+}
+
+constexpr int PREF_DEPTH = 4;
+using PrefQueue = RowQueue<2, PREF_DEPTH>;
+
+__device__ __forceinline__ void pref_fetch(const PrefArgs& a, const PrefQueue& rows, int slot,
+                                           int32_t t, int32_t s1, uint32_t m) {
+  if (__any_sync(0xffffffffu, m != 0)) {
+    if (t < s1) {
+      rows.copy(slot, 0, a.logp + t, s1 - t);
+      if (a.ref_logp) rows.copy(slot, 1, a.ref_logp + t, s1 - t);
+    }
+  }
+  rows.commit();
+}
+
+__device__ __forceinline__ void pref_sums(const PrefArgs& a, const PrefQueue& queue, int32_t span_i,
+                                          int lane) {
   const SeqLayout& q = a.seq;
-  const int32_t s0 = static_cast<int32_t>(span_i * a.span);
-  const int32_t s1 = static_cast<int32_t>(min(static_cast<int64_t>(s0) + a.span,
-                                              static_cast<int64_t>(q.N)));
-  Cursor c = cursor_at(q, s0);
+  const int32_t s0 = span_i * a.span, s1 = q.N - s0 < a.span ? q.N : s0 + a.span;
+  uint32_t ahead[PREF_DEPTH + 1];            // masks of the next rows
+#pragma unroll
+  for (int k = 0; k <= PREF_DEPTH; ++k) ahead[k] = load_mask4(a.mask, s0 + 128 * k + 4 * lane, s1);
+#pragma unroll
+  for (int k = 0; k < PREF_DEPTH; ++k)
+    pref_fetch(a, queue, k, s0 + 128 * k + 4 * lane, s1, ahead[k]);
+  Cursor c = cursor_at_warp(q, s0, lane);
   bool begun = c.b >= 0 && c.b < q.S && seq_begin(q, c.b) >= s0;
   double sum = 0.0;
   uint32_t n = 0;
+  int slot = 0;
   for (int32_t r = s0; r < s1 && c.b < q.S; r += 128) {
     const int32_t r1 = min(r + 128, s1), t = r + 4 * lane;
-    float x[4], y[4];
-    uint32_t m = 0;
-    if (t < s1) {
-      m = load_mask4(a.mask, t, q.N);
-      load4(a.logp, t, q.N, 0.f, x);
-      if (a.ref_logp) load4(a.ref_logp, t, q.N, 0.f, y);
+    const uint32_t m = ahead[0];
+#pragma unroll
+    for (int k = 0; k < PREF_DEPTH; ++k) ahead[k] = ahead[k + 1];
+    ahead[PREF_DEPTH] = load_mask4(a.mask, t + 128 * (PREF_DEPTH + 1), s1);
+    queue.wait();
+    const bool any = __any_sync(0xffffffffu, m != 0);
+    float x[4] = {}, y[4] = {};
+    if (any) {
+      queue.read(slot, 0, x);
+      if (a.ref_logp) queue.read(slot, 1, y);
     }
     double d[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      d[j] = (m >> j) & 1u ? static_cast<double>(x[j]) - (a.ref_logp ? static_cast<double>(y[j]) : 0.0)
-                           : 0.0;
+    for (int j = 0; j < 4; ++j) {
+      const double ref = a.ref_logp ? static_cast<double>(y[j]) : 0.0;
+      d[j] = mask_byte(m, j) ? static_cast<double>(x[j]) - ref : 0.0;
+    }
+    pref_fetch(a, queue, slot, t + 128 * PREF_DEPTH, s1, ahead[PREF_DEPTH - 1]);
+    if (++slot == PREF_DEPTH) slot = 0;
     if (c.e >= r1 && c.b >= 0) {             // the whole row belongs to one sequence
-      sum += (d[0] + d[1]) + (d[2] + d[3]);
-      n += __popc(m);
+      if (any) {
+        sum += (d[0] + d[1]) + (d[2] + d[3]);
+        n += __popc(byte_flags(m));
+      }
     } else {
       int32_t pos = r;
       while (pos < r1) {
@@ -394,7 +715,7 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t span_i, int
           for (int j = 0; j < 4; ++j)
             if (t + j >= pos && t + j < stop) {
               sum += d[j];
-              n += (m >> j) & 1u;
+              n += mask_byte(m, j) ? 1u : 0u;
             }
         }
         if (c.e >= r1) break;                // the row's rest is taken
@@ -402,7 +723,7 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t span_i, int
         sum = 0.0;
         n = 0;
         pos = max(stop, pos + 1);            // a bad cu still moves on
-        c = cursor_at(q, pos);
+        c = next_cursor(q, c, pos, lane);
         begun = true;
         if (c.b >= q.S) break;               // behind the last sequence
       }
@@ -413,7 +734,7 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t span_i, int
       sum = 0.0;
       n = 0;
       if (r1 >= s1) return;
-      c = cursor_at(q, r1);
+      c = next_cursor(q, c, r1, lane);
       begun = true;
     }
   }
@@ -468,42 +789,51 @@ __device__ __forceinline__ double pref_pair(const PrefArgs& a, int32_t i, int la
   return loss;
 }
 
-// The gradient of this thread's groups of four tokens.
-__device__ __forceinline__ void pref_tokens(const PrefArgs& a, int64_t thread, int64_t n_threads) {
+// The gradient of rows of 128 tokens, `row` and every n_warps-th after it;
+// m_next is the mask of the first.
+__device__ __forceinline__ void pref_tokens(const PrefArgs& a, int32_t row, int32_t n_warps,
+                                            uint32_t m_next, int lane) {
   const SeqLayout& q = a.seq;
-  const int64_t groups = (static_cast<int64_t>(q.N) + 3) / 4;
-  for (int64_t g = thread; g < groups; g += n_threads) {
-    const int32_t t0 = static_cast<int32_t>(4 * g);
-    const uint32_t m = load_mask4(a.mask, t0, q.N);
-    float out[4], k = 0.f;
-    Cursor c{-1, INT_MIN};
+  const int32_t n_rows = rows_of(q);
+  for (; row < n_rows; row += n_warps) {
+    const uint32_t m = m_next;
+    const int32_t row0 = row * 128, t0 = row0 + 4 * lane;
+    if (row + n_warps < n_rows) m_next = load_mask4(a.mask, (row + n_warps) * 128 + 4 * lane, q.N);
+    const Cursor c = cursor_at_warp(q, row0, lane);
+    float k = c.b >= 0 && c.b < q.S ? __ldcg(a.coef + c.b) : 0.f;
+    float out[4];
+    if (c.e >= row0 + 128) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      out[j] = 0.f;
-      if (!((m >> j) & 1u)) continue;
-      if (t0 + j >= c.e) {
-        c = cursor_at(q, t0 + j);
-        k = c.b >= 0 && c.b < q.S ? __ldcg(a.coef + c.b) : 0.f;
+      for (int j = 0; j < 4; ++j) out[j] = mask_byte(m, j) ? k : 0.f;
+    } else {
+      Cursor l = c;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (t0 + j >= l.e && t0 + j < q.N) {
+          l = cursor_at(q, t0 + j);
+          k = l.b >= 0 && l.b < q.S ? __ldcg(a.coef + l.b) : 0.f;
+        }
+        out[j] = mask_byte(m, j) ? k : 0.f;
       }
-      out[j] = k;
     }
-    store4(a.dlogp, t0, q.N, out);
+    if (t0 < q.N) store4(a.dlogp, t0, q.N, out);
   }
 }
 
-__global__ void __launch_bounds__(OBJ_THREADS) pref_sums_kernel(const PrefArgs a) {
+__global__ void __launch_bounds__(OBJ_THREADS, PREF_BLOCKS_PER_SM)
+pref_sums_kernel(const PrefArgs a) {
+  __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PrefQueue::WARP];
   griddep_launch_dependents();
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *a.status = 0u;
-    *a.ticket = 0u;
-  }
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * (OBJ_THREADS / 32) + (threadIdx.x >> 5);
-  if (i < a.n_spans) pref_sums(a, i, threadIdx.x & 31);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
+  const int warp = threadIdx.x >> 5;
+  const int32_t i = blockIdx.x * (OBJ_THREADS / 32) + warp;
+  const PrefQueue queue{rows + warp * PrefQueue::WARP + 16 * (threadIdx.x & 31)};
+  if (i < a.n_spans) pref_sums(a, queue, i, threadIdx.x & 31);
+  queue.drain();
 }
 
 __global__ void __launch_bounds__(OBJ_THREADS) pref_pair_kernel(const PrefArgs a) {
-  __shared__ double sm[32];
-  __shared__ uint32_t flag;
+  __shared__ double sm[OBJ_THREADS / 32];
   griddep_launch_dependents();
   griddep_wait();                            // the sums
   check_layout(a.seq, a.status);
@@ -516,36 +846,48 @@ __global__ void __launch_bounds__(OBJ_THREADS) pref_pair_kernel(const PrefArgs a
   }
   block_sum(v, sm);
   if (threadIdx.x == 0) a.partials[blockIdx.x] = v[0];
-  if (!last_block(a.ticket, &flag)) return;
-  v[0] = 0.0;
-  for (uint32_t k = threadIdx.x; k < gridDim.x; k += blockDim.x) v[0] += __ldcg(a.partials + k);
+}
+
+// The tokens' gradients, and in the last block the sum of the pairs' losses
+// (n_partials blocks of the kernel before), which the gradients do not need.
+__global__ void __launch_bounds__(OBJ_THREADS) pref_tokens_kernel(const PrefArgs a,
+                                                                  int n_partials) {
+  __shared__ double sm[OBJ_THREADS / 32];
+  const int lane = threadIdx.x & 31;
+  const int32_t row = (blockIdx.x * OBJ_THREADS + threadIdx.x) >> 5;
+  const uint32_t m = row < rows_of(a.seq) ? load_mask4(a.mask, row * 128 + 4 * lane, a.seq.N) : 0u;
+  griddep_wait();                            // the pairs
+  if (a.dlogp) pref_tokens(a, row, (gridDim.x * OBJ_THREADS) >> 5, m, lane);
+  if (blockIdx.x != gridDim.x - 1) return;
+  double v[1] = {0.0};
+  for (int k = threadIdx.x; k < n_partials; k += OBJ_THREADS) v[0] += __ldcg(a.partials + k);
   block_sum(v, sm);
   if (threadIdx.x == 0) *a.loss = static_cast<float>(v[0] * a.inv_pairs);
 }
 
-__global__ void __launch_bounds__(OBJ_THREADS) pref_tokens_kernel(const PrefArgs a) {
-  griddep_wait();                            // the pairs' gradients
-  pref_tokens(a, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
-              static_cast<int64_t>(gridDim.x) * blockDim.x);
-}
-
 // The three steps in one block, for batches where launches cost more than the
 // tokens.
-__global__ void __launch_bounds__(1024) pref_one_kernel(const PrefArgs a) {
-  __shared__ double sm[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+__global__ void __launch_bounds__(OBJ_THREADS) pref_one_kernel(const PrefArgs a) {
+  __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PrefQueue::WARP];
+  __shared__ double sm[OBJ_THREADS / 32];
+  constexpr int NW = OBJ_THREADS / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PrefQueue queue{rows + warp * PrefQueue::WARP + 16 * (threadIdx.x & 31)};
   if (threadIdx.x == 0) *a.status = 0u;
-  for (int64_t i = warp; i < a.n_spans; i += nw) pref_sums(a, i, lane);
+  for (int32_t i = warp; i < a.n_spans; i += NW) {
+    pref_sums(a, queue, i, lane);
+    queue.drain();
+  }
   __syncthreads();
   check_layout(a.seq, a.status);
   double v[1] = {0.0};
-  for (int32_t i = warp; i < a.seq.S / 2; i += nw) {
+  for (int32_t i = warp; i < a.seq.S / 2; i += NW) {
     const double l = pref_pair(a, i, lane);
     if (lane == 0) v[0] += l;
   }
   block_sum(v, sm);                          // its barriers also publish the gradients
   if (threadIdx.x == 0) *a.loss = static_cast<float>(v[0] * a.inv_pairs);
-  if (a.dlogp) pref_tokens(a, threadIdx.x, blockDim.x);
+  if (a.dlogp) pref_tokens(a, warp, NW, load_mask4(a.mask, 4 * threadIdx.x, a.seq.N), lane);
 }
 
 // ----------------------------------------------------------------------------
@@ -554,11 +896,11 @@ __global__ void __launch_bounds__(1024) pref_one_kernel(const PrefArgs a) {
 namespace {
 
 // Batches of at most this many tokens (and sequences) run in one block.
-constexpr int64_t ONE_BLOCK_TOKENS = 8192;
+constexpr int64_t ONE_BLOCK_TOKENS = 4096;
 
-template <typename Args>
-cudaError_t launch(void (*kern)(Args), int64_t blocks, int threads, cudaStream_t s,
-                   const Args& a, bool pdl) {
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kern)(KArgs...), int64_t blocks, int threads, cudaStream_t s, bool pdl,
+                   const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(threads);
@@ -568,7 +910,7 @@ cudaError_t launch(void (*kern)(Args), int64_t blocks, int threads, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   count_launch();
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -578,43 +920,66 @@ int64_t at_most(int64_t x, int64_t cap) { return x < cap ? (x > 0 ? x : 1) : cap
 
 }  // namespace
 
-kd_status policy_loss(const PolicyArgs& a, cudaStream_t s, int num_sms) {
+namespace {
+
+template <bool OLD, bool REF>
+kd_status policy_launch(PolicyArgs a, cudaStream_t s, int num_sms) {
   const SeqLayout& q = a.seq;
   if (q.N <= ONE_BLOCK_TOKENS && q.S <= ONE_BLOCK_TOKENS)
-    return launch(policy_one_kernel, 1, 1024, s, a, false) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
-  const bool counts = a.mask && a.reduction != KD_REDUCE_FIXED;
-  const size_t clear = OBJ_HEADER + (counts && a.reduction == KD_REDUCE_SEQUENCE
-                                         ? sizeof(uint32_t) * static_cast<size_t>(q.S) : 0);
-  if (cudaMemsetAsync(a.status, 0, clear, s) != cudaSuccess) return KD_ERR_CUDA;
-  if (counts) {
-    const int64_t blocks = (static_cast<int64_t>(q.N) + 4095) / 4096;
-    if (launch(policy_count_kernel, at_most(blocks, 4 * num_sms), OBJ_THREADS, s, a, false) !=
-        cudaSuccess)
-      return KD_ERR_CUDA;
+    return launch(policy_one_kernel<OLD, REF>, 1, OBJ_THREADS, s, false, a) == cudaSuccess
+               ? KD_OK
+               : KD_ERR_CUDA;
+  const bool all = a.mask && a.reduction == KD_REDUCE_TOKEN;
+  const bool each = a.mask && a.reduction == KD_REDUCE_SEQUENCE;
+  cudaError_t e = cudaSuccess;
+  if (all) {
+    a.n_counts = static_cast<int32_t>(
+        at_most((static_cast<int64_t>(q.N) + 16 * OBJ_THREADS - 1) / (16 * OBJ_THREADS),
+                at_most(4 * num_sms, OBJ_MAX_COUNTS)));
+    e = launch(policy_count_all_kernel, a.n_counts, OBJ_THREADS, s, false, a);
+  } else {
+    // status, ticket and, right behind them, the sequences' counts
+    e = cudaMemsetAsync(a.status, 0,
+                        OBJ_HEADER + (each ? sizeof(uint32_t) * static_cast<size_t>(q.S) : 0), s);
+    if (e == cudaSuccess && each)
+      e = launch(policy_count_each_kernel,
+                 at_most((static_cast<int64_t>(q.N) + 4095) / 4096, 4 * num_sms), OBJ_THREADS, s,
+                 false, a);
   }
-  const int64_t groups = (static_cast<int64_t>(q.N) + 3) / 4;
-  const int64_t cap = at_most(6 * num_sms, OBJ_MAX_BLOCKS);
-  if (launch(policy_main_kernel, at_most((groups + OBJ_THREADS - 1) / OBJ_THREADS, cap),
-             OBJ_THREADS, s, a, counts) != cudaSuccess)
-    return KD_ERR_CUDA;
-  return KD_OK;
+  if (e != cudaSuccess) return KD_ERR_CUDA;
+  const int64_t per_block = 4 * OBJ_THREADS;
+  const int64_t cap = at_most(POLICY_BLOCKS_PER_SM * num_sms, OBJ_MAX_BLOCKS);
+  e = launch(policy_main_kernel<OLD, REF>, at_most((q.N + per_block - 1) / per_block, cap),
+             OBJ_THREADS, s, all || each, a);
+  return e == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+}
+
+}  // namespace
+
+kd_status policy_loss(const PolicyArgs& a, cudaStream_t s, int num_sms) {
+  if (a.old_logp)
+    return a.ref_logp ? policy_launch<true, true>(a, s, num_sms)
+                      : policy_launch<true, false>(a, s, num_sms);
+  return a.ref_logp ? policy_launch<false, true>(a, s, num_sms)
+                    : policy_launch<false, false>(a, s, num_sms);
 }
 
 kd_status preference_loss(const PrefArgs& a, cudaStream_t s, int num_sms) {
   const SeqLayout& q = a.seq;
   if (q.N <= ONE_BLOCK_TOKENS && q.S <= ONE_BLOCK_TOKENS)
-    return launch(pref_one_kernel, 1, 1024, s, a, false) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+    return launch(pref_one_kernel, 1, OBJ_THREADS, s, false, a) == cudaSuccess ? KD_OK
+                                                                                    : KD_ERR_CUDA;
   constexpr int W = OBJ_THREADS / 32;
-  if (launch(pref_sums_kernel, (a.n_spans + W - 1) / W, OBJ_THREADS, s, a, false) != cudaSuccess)
+  if (launch(pref_sums_kernel, (a.n_spans + W - 1) / W, OBJ_THREADS, s, false, a) != cudaSuccess)
     return KD_ERR_CUDA;
-  const int64_t pairs = q.S / 2, cap = at_most(8 * num_sms, OBJ_MAX_BLOCKS);
-  if (launch(pref_pair_kernel, at_most((pairs + W - 1) / W, cap), OBJ_THREADS, s, a, true) !=
+  const int64_t cap = at_most(8 * num_sms, OBJ_MAX_BLOCKS);
+  const int64_t pair_blocks = at_most((q.S / 2 + W - 1) / W, cap);
+  if (launch(pref_pair_kernel, pair_blocks, OBJ_THREADS, s, true, a) != cudaSuccess)
+    return KD_ERR_CUDA;
+  const int64_t per_block = 4 * OBJ_THREADS;
+  const int64_t blocks = a.dlogp ? at_most((q.N + per_block - 1) / per_block, cap) : 1;
+  if (launch(pref_tokens_kernel, blocks, OBJ_THREADS, s, true, a, static_cast<int>(pair_blocks)) !=
       cudaSuccess)
-    return KD_ERR_CUDA;
-  if (!a.dlogp) return KD_OK;
-  const int64_t groups = (static_cast<int64_t>(q.N) + 3) / 4;
-  if (launch(pref_tokens_kernel, at_most((groups + OBJ_THREADS - 1) / OBJ_THREADS, cap),
-             OBJ_THREADS, s, a, true) != cudaSuccess)
     return KD_ERR_CUDA;
   return KD_OK;
 }

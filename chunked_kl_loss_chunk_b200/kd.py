@@ -485,7 +485,13 @@ class FusedTopKKLLoss(torch.autograd.Function):
 
 def _require(name: str, t, dtype, shape, device):
     """Checks one tensor argument: a dense CUDA tensor of this type and shape on
-    this device."""
+    this device.  (The usual case first: these checks are a good part of what a
+    call on a small batch costs.)"""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: a torch tensor is needed")
     if t.dtype is not dtype:
@@ -494,8 +500,7 @@ def _require(name: str, t, dtype, shape, device):
         raise ValueError(f"{name}: shape {tuple(shape)} is needed, not {tuple(t.shape)}")
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name}: on {t.device}, not on the CUDA device {device} of the call")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    raise ValueError(f"{name}: must be contiguous")
 
 
 _HERE = contextlib.nullcontext()
@@ -513,8 +518,19 @@ def _use_stream(device, stream):
 
 
 def _current_stream(device) -> int:
-    # by the device's index: looking up an unnamed current device costs more than the launch
-    return torch.cuda.current_stream(device.index).cuda_stream
+    # the raw handle: building a torch.cuda.Stream for it costs as much as the launch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _workspace(ws, nbytes: int, like):
+    """(what to keep alive, address, bytes) of a call's workspace: the given one,
+    or one allocated on the device of the fp32 or bf16 tensor `like`."""
+    if ws is not None:
+        _require("ws", ws, torch.uint8, (ws.numel(),), like.device)
+        return ws, ws.data_ptr(), ws.numel()
+    n = max(nbytes, 1024)
+    buf = like.new_empty((n + 1024) // 2)
+    return buf, (buf.data_ptr() + 1023) & ~1023, n
 
 
 def _head_sizes(h, W, targets):
@@ -542,8 +558,10 @@ def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, 
         if ws is None:
             ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, int(backward)),
                                  h.device)
+        else:
+            _require("ws", ws, torch.uint8, (ws.numel(),), h.device)
         logp = torch.empty((T,), dtype=torch.float32, device=h.device)
-        lse = torch.empty((T,), dtype=torch.float32, device=h.device)
+        lse = torch.empty_like(logp)
         _check(kd_head_logprob_fwd(h.data_ptr(), W.data_ptr(), code, T, d, V, targets.data_ptr(),
                                    chunk, float(temperature), logp.data_ptr(), lse.data_ptr(),
                                    ws.data_ptr(), ws.numel(), _current_stream(h.device)),
@@ -576,6 +594,8 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
     with _use_stream(h.device, stream):
         if ws is None:
             ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, 1), h.device)
+        else:
+            _require("ws", ws, torch.uint8, (ws.numel(),), h.device)
         if not need[0]:
             dH = None
         elif dH is None:
@@ -646,14 +666,6 @@ def _sequences(logp, cu_seqlens, mask):
     return n_seqs, logp.numel()
 
 
-def _scratch(nbytes: int, like):
-    """Workspace of one call on the device of the fp32 or bf16 tensor `like`: (the
-    buffer to keep, its aligned address, bytes)."""
-    n = max(int(nbytes), 1024)
-    buf = like.new_empty((n + 1024) // 2)
-    return buf, (buf.data_ptr() + 1023) & ~1023, n
-
-
 def policy_loss(logp, old_logp, advantages, *, mask=None, ref_logp=None, cu_seqlens=None,
                 advantages_per: str = "sequence", clip_low: float = 0.2, clip_high: float = 0.2,
                 kl_coef: float = 0.0, reduction: str = "token", denom: float | None = None,
@@ -682,19 +694,17 @@ def policy_loss(logp, old_logp, advantages, *, mask=None, ref_logp=None, cu_seql
         _require("old_logp", old_logp, torch.float32, logp.shape, dev)
     if ref_logp is not None:
         _require("ref_logp", ref_logp, torch.float32, logp.shape, dev)
+    lib = load()
     with _use_stream(dev, stream):
-        if ws is None:
-            keep, at, nbytes = _scratch(kd_policy_loss_workspace_size(n_seqs, n), logp)
-        else:
-            at, nbytes = ws.data_ptr(), ws.numel()
+        keep, at, nbytes = _workspace(ws, lib.kd_policy_loss_workspace_size(n_seqs, n), logp)
         loss = logp.new_empty(())
         stats = logp.new_empty(4)
         dlogp = torch.empty_like(logp) if grad else None
-        _check(kd_policy_loss(logp.data_ptr(), _ptr(old_logp), _ptr(ref_logp), advantages.data_ptr(),
-                              int(per_token), _ptr(mask), _ptr(cu_seqlens), n_seqs, n, clip_low,
-                              clip_high, kl_coef, REDUCTIONS[reduction],
-                              0.0 if denom is None else denom, loss.data_ptr(), stats.data_ptr(),
-                              _ptr(dlogp), at, nbytes, _current_stream(dev)),
+        _check(lib.kd_policy_loss(logp.data_ptr(), _ptr(old_logp), _ptr(ref_logp),
+                                  advantages.data_ptr(), per_token, _ptr(mask), _ptr(cu_seqlens),
+                                  n_seqs, n, clip_low, clip_high, kl_coef, REDUCTIONS[reduction],
+                                  0.0 if denom is None else denom, loss.data_ptr(),
+                                  stats.data_ptr(), _ptr(dlogp), at, nbytes, _current_stream(dev)),
                "kd_policy_loss")
     return loss, stats, dlogp
 
@@ -739,19 +749,18 @@ def preference_loss(logp, *, ref_logp=None, mask=None, cu_seqlens=None, kind: st
     if ref_logp is not None:
         _require("ref_logp", ref_logp, torch.float32, logp.shape, dev)
     pairs = n_seqs // 2
+    lib = load()
     with _use_stream(dev, stream):
-        if ws is None:
-            keep, at, nbytes = _scratch(kd_preference_loss_workspace_size(pairs, n), logp)
-        else:
-            at, nbytes = ws.data_ptr(), ws.numel()
+        keep, at, nbytes = _workspace(ws, lib.kd_preference_loss_workspace_size(pairs, n), logp)
         loss = logp.new_empty(())
         rewards = logp.new_empty(n_seqs)
         dlogp = torch.empty_like(logp) if grad else None
-        _check(kd_preference_loss(logp.data_ptr(), _ptr(ref_logp), _ptr(mask), _ptr(cu_seqlens), pairs, n,
-                                  PREFERENCE_KINDS[kind], beta, margin, label_smoothing,
-                                  int(length_normalize), pairs if pairs_total is None else pairs_total,
-                                  loss.data_ptr(), rewards.data_ptr(), _ptr(dlogp), at, nbytes,
-                                  _current_stream(dev)),
+        _check(lib.kd_preference_loss(logp.data_ptr(), _ptr(ref_logp), _ptr(mask), _ptr(cu_seqlens),
+                                      pairs, n, PREFERENCE_KINDS[kind], beta, margin,
+                                      label_smoothing, bool(length_normalize),
+                                      pairs if pairs_total is None else pairs_total,
+                                      loss.data_ptr(), rewards.data_ptr(), _ptr(dlogp), at, nbytes,
+                                      _current_stream(dev)),
                "kd_preference_loss")
     return loss, rewards, dlogp
 
@@ -804,10 +813,11 @@ def grad_sumsq(grads, stream=None):
     """Sum of squares of a list of gradients, fp64 [] (its root is their norm)."""
     grads = list(grads)
     n, dev, ptrs, sizes, codes = _grad_arrays("grads", grads)
+    lib = load()
     with _use_stream(dev, stream):
-        keep, at, nbytes = _scratch(kd_grad_clip_workspace_size(n), grads[0])
+        keep, at, nbytes = _workspace(None, lib.kd_grad_clip_workspace_size(n), grads[0])
         out = torch.empty((), dtype=torch.float64, device=dev)
-        _check(kd_grad_sumsq(ptrs.buffer_info()[0], sizes.buffer_info()[0], codes.buffer_info()[0], n,
+        _check(lib.kd_grad_sumsq(ptrs.buffer_info()[0], sizes.buffer_info()[0], codes.buffer_info()[0], n,
                              out.data_ptr(), at, nbytes, _current_stream(dev)),
                "kd_grad_sumsq")
     return out
@@ -829,10 +839,11 @@ def clip_grad_norm(grads, max_norm: float, out=None, sumsq=None, stream=None):
             raise ValueError("out: the sizes, types and device of grads are needed")
     if sumsq is not None:
         _require("sumsq", sumsq, torch.float64, (), dev)
+    lib = load()
     with _use_stream(dev, stream):
-        keep, at, nbytes = _scratch(kd_grad_clip_workspace_size(n), grads[0])
+        keep, at, nbytes = _workspace(None, lib.kd_grad_clip_workspace_size(n), grads[0])
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _check(kd_grad_clip(ptrs.buffer_info()[0], outs.buffer_info()[0], sizes.buffer_info()[0],
+        _check(lib.kd_grad_clip(ptrs.buffer_info()[0], outs.buffer_info()[0], sizes.buffer_info()[0],
                             codes.buffer_info()[0], n, max_norm, _ptr(sumsq), norm.data_ptr(), at,
                             nbytes, _current_stream(dev)),
                "kd_grad_clip")
