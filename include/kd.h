@@ -382,8 +382,10 @@ kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uin
 
 size_t kd_grad_clip_workspace_size(int n_tensors);
 
-/* *sumsq (device, double) = the sum of squares of all elements, added in fp64
- * in an order that depends on the sizes alone.  For norms over several ranks:
+/* *sumsq (device, double) = the sum of squares of all elements: 16 bytes' worth
+ * added in fp32 (in fp64 where squares leave its range), those sums in fp64, in
+ * an order that depends on the sizes and the device alone; off by at most 2^-21
+ * of the sum.  For norms over several ranks:
  * add the ranks' sums of the tensors that are split, then call kd_grad_clip. */
 kd_status kd_grad_sumsq(const void* const* grads, const int64_t* numels, const int* dtypes,
                         int n_tensors, double* sumsq, void* ws, size_t ws_bytes, void* stream);

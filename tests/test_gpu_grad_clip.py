@@ -1,8 +1,11 @@
 """GPU parity of the global gradient norm and clipping against fp64.
 
-Tolerances: squares are added in fp64, the norm is rounded to fp32 once
-(2^-24); the factor is rounded once, a product once more: 2^-22 of an fp32
-value; a bf16 one is rounded to half a step, 2^-8, besides.
+Tolerances: at most 8 squares are added in fp32, with as many roundings of
+2^-24 of a sum of positive terms, and the rest in fp64: 2^-21 of the sum of
+squares, half of it of the norm, which is rounded to fp32 once (2^-24); together
+below 2^-21 (NORM).  The factor has the norm's error and a rounding, a product one
+more: below 2^-20 of an fp32 value; a bf16 one is rounded to half a step, 2^-8,
+besides.
 """
 
 import math
@@ -16,6 +19,7 @@ from gpu_util import require_gpu
 pytestmark = pytest.mark.gpu
 
 F32, BF16 = torch.float32, torch.bfloat16
+NORM = 2.0 ** -21
 
 
 def _values(n, dtype, gen, scale=1.0):
@@ -24,7 +28,7 @@ def _values(n, dtype, gen, scale=1.0):
 
 def _check(got, src, c):
     want = src.double() * c
-    tol = 2.0 ** -22 + (2.0 ** -8 if src.dtype is BF16 else 0.0)
+    tol = 2.0 ** -20 + (2.0 ** -8 if src.dtype is BF16 else 0.0)
     assert got.dtype == src.dtype and got.shape == src.shape
     assert bool(((got.double() - want).abs() <= tol * want.abs() + 1e-40).all())
 
@@ -77,7 +81,7 @@ def test_norm_and_clipping(name, where):
             norm = kd.clip_grad_norm(grads, max_norm, out=outs)
             for p, t in zip(pads, grads):
                 assert bool((p[:shift] == 7).all()) and bool((p[shift + t.numel():] == 7).all())
-        assert abs(norm.item() - want) <= 2.0 ** -23 * want
+        assert abs(norm.item() - want) <= NORM * want
         for g, s in zip(outs[:300], src[:300]):
             _check(g, s, c)
             if c == 1.0:
@@ -86,18 +90,20 @@ def test_norm_and_clipping(name, where):
             keep = marks[dt] if where == "in-place" else torch.ones_like(marks[dt])
             assert torch.equal(flat[dt][keep], before[dt][keep])
     total = kd.grad_sumsq([s for s in src])
-    assert abs(total.item() - want * want) <= 1e-12 * want * want
+    assert abs(total.item() - want * want) <= 2.0 ** -21 * want * want
 
 
 def test_values_whose_squares_leave_fp32():
     require_gpu()
-    for scale in (1e30, 1e-30):
+    for scale in (1e30, 1e-30, 3e18, 3e-16, 1e-22):
         g = [torch.full((1000,), scale, device="cuda"), torch.full((5,), 2 * scale, device="cuda", dtype=BF16)]
         want = _norm(g)
         assert 0 < want < 1e33
+        mixed = [torch.tensor([scale, 1.0, 0.0, -scale, 0.0, 0.0, 0.0, 0.0, 1e-38], device="cuda")]
+        assert abs(kd.clip_grad_norm(mixed, math.inf).item() - _norm(mixed)) <= NORM * _norm(mixed)
         norm = kd.clip_grad_norm(g, 1.0)
-        assert abs(norm.item() - want) <= 2.0 ** -22 * want
-        assert abs(g[0][3].item() - scale * min(1.0, 1.0 / (want + 1e-6))) <= 2.0 ** -21 * abs(g[0][3].item())
+        assert abs(norm.item() - want) <= NORM * want
+        assert abs(g[0][3].item() - scale * min(1.0, 1.0 / (want + 1e-6))) <= 2.0 ** -19 * abs(g[0][3].item())
 
 
 def test_infinities_and_nan_follow_the_formula():
@@ -118,7 +124,7 @@ def test_offsets_past_32_bits():
     g[-1] = 2.0
     want = math.sqrt((n - 1) * 0.25 + 4.0)
     norm = kd.clip_grad_norm([g], want / 2)
-    assert abs(norm.item() - want) <= 2.0 ** -23 * want
+    assert abs(norm.item() - want) <= NORM * want
     assert g[-1].item() == 1.0 and g[-2].item() == 0.25 and g[0].item() == 0.25
     assert g.sum(dtype=torch.float64).item() == (n - 1) * 0.25 + 1.0
 
@@ -136,9 +142,9 @@ def test_same_bits_every_time_and_given_sum():
     part = [t.clone() for t in src]
     kd.clip_grad_norm(part[:1], 1.0, sumsq=total)
     norm = kd.clip_grad_norm(part[1:], 1.0, sumsq=total)
-    assert abs(norm.item() - norms[0].item()) <= 2.0 ** -23 * norm.item()
+    assert abs(norm.item() - norms[0].item()) <= 2 * NORM * norm.item()
     for a, b in zip(part, outs[0]):
-        assert bool(((a - b).abs() <= 2.0 ** -22 * b.abs()).all())
+        assert bool(((a - b).abs() <= 2.0 ** -19 * b.abs()).all())
 
 
 def test_captured_replay_and_another_stream():
