@@ -287,10 +287,11 @@ size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t c
 static kd_status validate_head(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                                int64_t V, const int32_t* targets, int64_t chunk, float tau,
                                void* ws, size_t ws_bytes, bool backward) {
-  // one entry per row: `targets` stands in for both arrays of a cache with K = 1
+  if (!targets || !aligned(targets, 4)) return KD_ERR_INVALID_ARG;
+  // the head's own checks, with h in the places of the two arrays of a cache with K = 1
   const kd_status st =
-      kd::validate_loss_inputs(h, W, dtype, T, d, V, reinterpret_cast<const float*>(targets),
-                               targets, 1, chunk, tau);
+      kd::validate_loss_inputs(h, W, dtype, T, d, V, static_cast<const float*>(h),
+                               static_cast<const int32_t*>(h), 1, chunk, tau);
   if (st != KD_OK) return st;
   if (!ws || !aligned(ws, kd::KD_WS_ALIGN)) return KD_ERR_INVALID_ARG;
   const kd::WsLayout L =
@@ -305,7 +306,7 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
   const kd_status st = validate_head(h, W, dtype, T, d, V, targets, chunk, temperature, ws,
                                      ws_bytes, false);
   if (st != KD_OK) return st;
-  if (!logp || !lse || !aligned(logp, 16) || !aligned(lse, 16)) return KD_ERR_INVALID_ARG;
+  if (!logp || !lse || !aligned(logp, 4) || !aligned(lse, 4)) return KD_ERR_INVALID_ARG;
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
   kd::RowTerms rt;
@@ -323,8 +324,8 @@ kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T
                                      ws_bytes, true);
   if (st != KD_OK) return st;
   if (!lse || !grad_logp || (!dH && !dW)) return KD_ERR_INVALID_ARG;
-  if (!aligned(lse, 16) || !aligned(grad_logp, 16) || !aligned(dH, 16) || !aligned(dW, 16) ||
-      (grad_loss && !aligned(grad_loss, 4)))
+  if (!aligned(lse, 4) || !aligned(grad_logp, 4) || !aligned(dH, 16) || !aligned(dW, 16) ||
+      !aligned(grad_loss, 4))
     return KD_ERR_INVALID_ARG;
   if (dW && dW_dtype != KD_DTYPE_F32 &&
       (dW_dtype != KD_DTYPE_BF16 || dtype != KD_DTYPE_BF16 || accumulate_dW ||
@@ -380,9 +381,9 @@ kd_status kd_policy_loss(const float* logp, const float* old_logp, const float* 
                          double denom, float* loss, float* stats, float* dlogp, void* ws,
                          size_t ws_bytes, void* stream) {
   if (!logp || !advantages || !loss || !stats || !ws) return KD_ERR_INVALID_ARG;
-  if (!aligned(logp, 16) || !aligned(old_logp, 16) || !aligned(ref_logp, 16) ||
-      !aligned(advantages, advantages_per_token ? 16 : 4) || !aligned(mask, 16) ||
-      !aligned(loss, 4) || !aligned(stats, 4) || !aligned(dlogp, 16) || !aligned(ws, 1024))
+  if (!aligned(logp, 4) || !aligned(old_logp, 4) || !aligned(ref_logp, 4) ||
+      !aligned(advantages, 4) || !aligned(loss, 4) || !aligned(stats, 4) || !aligned(dlogp, 4) ||
+      !aligned(ws, 1024))
     return KD_ERR_INVALID_ARG;
   if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0) || !isfinite(kl_coef) ||
       (kl_coef != 0.0 && !ref_logp))
@@ -401,6 +402,9 @@ kd_status kd_policy_loss(const float* logp, const float* old_logp, const float* 
   a.adv = advantages;
   a.mask = mask;
   a.adv_per_token = advantages_per_token != 0;
+  a.vec = aligned(logp, 16) && aligned(old_logp, 16) && aligned(ref_logp, 16) &&
+          (!a.adv_per_token || aligned(advantages, 16)) && aligned(dlogp, 16);
+  a.mask_vec = aligned(mask, 16);
   a.reduction = reduction;
   a.bound_hi = static_cast<float>(1.0 + clip_high);
   a.bound_lo = static_cast<float>(1.0 - clip_low);
@@ -441,8 +445,8 @@ kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uin
                              float* rewards, float* dlogp, void* ws, size_t ws_bytes,
                              void* stream) {
   if (!logp || !loss || !rewards || !ws) return KD_ERR_INVALID_ARG;
-  if (!aligned(logp, 16) || !aligned(ref_logp, 16) || !aligned(mask, 16) || !aligned(loss, 4) ||
-      !aligned(rewards, 4) || !aligned(dlogp, 16) || !aligned(ws, 1024))
+  if (!aligned(logp, 4) || !aligned(ref_logp, 4) || !aligned(loss, 4) || !aligned(rewards, 4) ||
+      !aligned(dlogp, 4) || !aligned(ws, 1024))
     return KD_ERR_INVALID_ARG;
   if (kind != KD_PREF_SIGMOID && kind != KD_PREF_HINGE && kind != KD_PREF_IPO)
     return KD_ERR_INVALID_ARG;
@@ -463,6 +467,8 @@ kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uin
   a.mask = mask;
   a.kind = kind;
   a.normalize = length_normalize != 0;
+  a.vec = aligned(logp, 16) && aligned(ref_logp, 16) && aligned(dlogp, 16);
+  a.mask_vec = aligned(mask, 16);
   a.beta = beta;
   a.margin = margin;
   a.smoothing = label_smoothing;

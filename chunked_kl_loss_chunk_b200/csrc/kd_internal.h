@@ -116,6 +116,7 @@ struct PolicyArgs {
   const float *logp, *old_logp, *ref_logp, *adv;
   const uint8_t* mask;
   int adv_per_token, reduction;
+  int vec, mask_vec;                // float arrays and mask 16-byte aligned
   float bound_hi, bound_lo;         // 1 + clip_high, 1 - clip_low
   float log_hi, log_lo;             // their logarithms, rounded, and exact:
   double log_hi64, log_lo64;
@@ -140,9 +141,11 @@ struct PrefArgs {
   const float *logp, *ref_logp;
   const uint8_t* mask;
   int kind, normalize;
+  int vec, mask_vec;                // float arrays and mask 16-byte aligned
   double beta, margin, smoothing, inv_pairs;
   int32_t span;                     // tokens a warp sums, a multiple of 128
   int32_t n_spans;
+  int32_t pairs_per_warp;
   float *loss, *rewards, *dlogp;
   uint32_t* status;
   SeqPart *whole, *head, *tail;     // [S], [n_spans], [n_spans]
@@ -150,7 +153,7 @@ struct PrefArgs {
   double* partials;
 };
 
-kd_status preference_loss(const PrefArgs& a, cudaStream_t s, int num_sms);
+kd_status preference_loss(PrefArgs a, cudaStream_t s, int num_sms);
 
 // Tokens a warp sums: one span for each of the warps that are resident at once
 // (32 an SM), in whole rows of 128.

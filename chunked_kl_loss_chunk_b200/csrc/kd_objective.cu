@@ -29,7 +29,8 @@ __device__ __forceinline__ int32_t seq_begin(const SeqLayout& q, int32_t b) {
 // t / L for 0 <= t < 2^31 by a multiplication (Granlund and Montgomery, "Division
 // by invariant integers using multiplication", 1994): the host gives ceil(2^p / L).
 __device__ __forceinline__ int32_t row_of(const SeqLayout& q, int32_t t) {
-  return q.L == 1 ? t : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(t), q.div_mul) >> q.div_shift);
+  if (q.L == 1) return t;
+  return static_cast<int32_t>(__umulhi(static_cast<uint32_t>(t), q.div_mul) >> q.div_shift);
 }
 
 // Sequence of token t: the last b with begin(b) <= t, so that empty sequences
@@ -67,13 +68,52 @@ struct Cursor {
   int32_t b, e;
 };
 __device__ __forceinline__ Cursor cursor_of(const SeqLayout& q, int32_t b) {
-  return Cursor{b, b >= q.S ? INT_MAX : seq_begin(q, b + 1)};   // b == -1: ends where the first begins
+  // b == -1 ends where the first sequence begins
+  return Cursor{b, b >= q.S ? INT_MAX : seq_begin(q, b + 1)};
 }
 __device__ __forceinline__ Cursor cursor_at(const SeqLayout& q, int32_t t) {
   return cursor_of(q, seq_of(q, t));
 }
 __device__ __forceinline__ Cursor cursor_at_warp(const SeqLayout& q, int32_t t, int lane) {
   return cursor_of(q, seq_of_warp(q, t, lane));
+}
+
+// The sequence of token t, which c ends at or before: the next, unless that is empty.
+__device__ __forceinline__ Cursor cursor_after(const SeqLayout& q, const Cursor& c, int32_t t) {
+  if (c.b + 1 < q.S) {
+    const int32_t e = seq_begin(q, c.b + 2);
+    if (e > t) return Cursor{c.b + 1, e};
+  }
+  return cursor_at(q, t);
+}
+
+// Sequences of a lane's four tokens of a row in which c, its first token's, ends:
+// the beginnings of the next 32 are loaded once and searched by shuffles; only a
+// row with more has each lane search cu.
+__device__ __forceinline__ void row_sequences(const SeqLayout& q, const Cursor& c, int32_t row0,
+                                              int lane, int32_t (&b)[4]) {
+  const int32_t last = min(row0 + 127, q.N - 1), t0 = row0 + 4 * lane;
+  if (!q.cu) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = row_of(q, min(t0 + j, last));
+    return;
+  }
+  const int64_t next = static_cast<int64_t>(c.b) + 1 + lane;
+  const int32_t start = next <= q.S ? seq_begin(q, static_cast<int32_t>(next)) : INT_MAX;
+  const bool few = __shfl_sync(0xffffffffu, start, 31) > last;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int32_t t = min(t0 + j, last);
+    if (few) {
+      int k = 0;                           // beginnings at or before t
+#pragma unroll
+      for (int step = 16; step > 0; step >>= 1)
+        if (__shfl_sync(0xffffffffu, start, k + step - 1) <= t) k += step;
+      b[j] = c.b + k;
+    } else {
+      b[j] = seq_of(q, t);
+    }
+  }
 }
 
 // Records KD_ERR_BAD_INDEX unless 0 <= cu[0] <= cu[1] <= ... <= cu[S] <= N.
@@ -89,8 +129,8 @@ __device__ __forceinline__ void check_layout(const SeqLayout& q, uint32_t* statu
 
 // ----------------------------------------------------------------------------
 // Rows of 128 tokens, four a lane, copied asynchronously into shared memory some
-// rows ahead of their use.  A lane copies and reads its own tokens alone, so the
-// copies need no barrier.  With the loads of the next row held in registers
+// rows ahead of their use.  A lane copies its own tokens, and as a rule reads no
+// others, so the copies need no barrier.  With the loads of the next row held in registers
 // instead, the sums of the preference loss over 4.2M tokens took 15 us, waiting for
 // memory at 28 warps an SM; they take 10 us.  The mask is loaded one row further
 // ahead, into registers, and a row in which no token counts (a prompt, padding) is
@@ -103,12 +143,20 @@ struct RowQueue {
   unsigned char* at;                                  // this lane's places
 
   // The four values from p, of which the first `left` lie in the array; 0 in the places of
-  // the others.
-  __device__ __forceinline__ void copy(int slot, int k, const float* p, int left) const {
+  // the others.  vec: p is 16-byte aligned.
+  __device__ __forceinline__ void copy(int slot, int k, const float* p, int left, bool vec) const {
     const uint32_t to = smem_u32(at + slot * ROW + k * 512);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p),
-                 "r"(left < 4 ? 4 * left : 16)
-                 : "memory");
+    if (vec) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p),
+                   "r"(left < 4 ? 4 * left : 16)
+                   : "memory");
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * j),
+                     "l"(j < left ? p + j : p), "r"(j < left ? 4 : 0)
+                     : "memory");
+    }
   }
   __device__ __forceinline__ void commit() const {
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -141,20 +189,22 @@ __device__ __forceinline__ uint32_t byte_flags(uint32_t w) {
   return (((w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w) & 0x80808080u;
 }
 
-// Mask bytes of four tokens, straight from memory.
-__device__ __forceinline__ uint32_t load_mask4(const uint8_t* p, int32_t t, int32_t N) {
+// Mask bytes of four tokens, straight from memory.  vec: p is 4-byte aligned.
+__device__ __forceinline__ uint32_t load_mask4(const uint8_t* p, int32_t t, int32_t N, bool vec) {
   if (t >= N) return 0u;
   if (!p) return t + 4 <= N ? 0x01010101u : 0x01010101u >> (8 * (4 - (N - t)));
-  if (t + 4 <= N) return __ldg(reinterpret_cast<const uint32_t*>(p + t));
+  if (vec && t + 4 <= N) return __ldg(reinterpret_cast<const uint32_t*>(p + t));
   uint32_t m = 0;
-  for (int j = 0; j < N - t; ++j) m |= static_cast<uint32_t>(__ldg(p + t + j)) << (8 * j);
+  for (int j = 0; j < min(N - t, 4); ++j) m |= static_cast<uint32_t>(__ldg(p + t + j)) << (8 * j);
   return m;
 }
 
 __device__ __forceinline__ int32_t rows_of(const SeqLayout& q) { return (q.N + 127) / 128; }
 
-__device__ __forceinline__ void store4(float* p, int32_t t, int32_t N, const float (&v)[4]) {
-  if (t + 4 <= N) {
+// Four tokens' values to p + t.  vec: p is 16-byte aligned.
+__device__ __forceinline__ void store4(float* p, int32_t t, int32_t N, const float (&v)[4],
+                                       bool vec) {
+  if (vec && t + 4 <= N) {
     *reinterpret_cast<float4*>(p + t) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
 #pragma unroll
@@ -188,6 +238,7 @@ __device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t* sm_flag) 
 constexpr int OBJ_THREADS = 256;
 constexpr int POLICY_STATS = 5;   // sums: loss, tokens, r, clipped, KL
 constexpr int PREF_BLOCKS_PER_SM = 4;
+constexpr int PREF_SHORT_MEAN = 30;   // tokens a sequence, on average, below which it is short
 constexpr int POLICY_BLOCKS_PER_SM = 3;
 
 // Two fp32 values that one instruction works on (fma.rn.f32x2 and its like): the
@@ -251,7 +302,7 @@ __device__ __forceinline__ F2 exp_minus_linear(const F2& q) {
 // Number of the 16 tokens from t0 that the mask keeps, as bits.
 __device__ __forceinline__ uint32_t mask_bits16(const PolicyArgs& a, int32_t t0) {
   uint32_t m = 0;
-  if (t0 + 16 <= a.seq.N) {
+  if (a.mask_vec && t0 + 16 <= a.seq.N) {
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.mask + t0));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -293,50 +344,61 @@ __device__ __forceinline__ uint32_t block_count(uint32_t n, uint32_t* sm) {
   return n;
 }
 
+__device__ __forceinline__ void policy_count_flush(const PolicyArgs& a, int32_t b, uint32_t n,
+                                                   int lane) {
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0 && n && b >= 0 && b < a.seq.S) atomicAdd(a.count + b, n);
+}
+
 // Unmasked tokens of each sequence, added to count[b] (zero before).  A warp takes
-// 512 tokens at a time; integer atomics, whose order does not matter.
+// 512 tokens at a time, and holds its count while the sequence stays the same: atomics
+// on one address queue up.  (They are integer ones; their order does not matter.)
 __device__ __forceinline__ void policy_count_each(const PolicyArgs& a, int32_t warp,
                                                   int32_t n_warps, int lane) {
   const SeqLayout& q = a.seq;
+  int32_t held_b = -1;
+  uint32_t held = 0;
   for (int64_t row = static_cast<int64_t>(warp) * 512; row < q.N;
        row += static_cast<int64_t>(n_warps) * 512) {
-    const int32_t t0 = static_cast<int32_t>(row) + lane * 16;    // row + 512 <= N + 511 < 2^31
+    const int32_t r0 = static_cast<int32_t>(row), t0 = r0 + lane * 16;   // below N + 512 < 2^31
     const uint32_t m = mask_bits16(a, t0);
-    // the row's sequence; a lane looks up its own where the row's ends before it
-    Cursor c = cursor_at_warp(q, static_cast<int32_t>(row), lane);
-    if (t0 >= c.e && t0 < q.N) c = cursor_at(q, t0);
-    int same;
-    __match_all_sync(0xffffffffu, c.e >= t0 + 16 ? c.b : -2 - lane, &same);
-    if (same) {
-      const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(m));
-      if (lane == 0 && n && c.b >= 0 && c.b < q.S) atomicAdd(a.count + c.b, n);
-    } else {
-      int32_t pos = t0;
-      const int32_t end = min(t0 + 16, q.N);
-      while (pos < end) {
-        const int32_t stop = max(min(c.e, end), pos + 1);   // a bad cu still moves on
-        const uint32_t n = __popc((m >> (pos - t0)) & ((1u << (stop - pos)) - 1u));
-        if (n && c.b >= 0 && c.b < q.S) atomicAdd(a.count + c.b, n);
-        pos = stop;
-        if (pos < end) c = cursor_at(q, pos);
+    const Cursor first = cursor_at_warp(q, r0, lane);
+    if (first.e >= min(r0 + 512, q.N)) {       // one sequence holds the 512
+      if (first.b != held_b) {
+        policy_count_flush(a, held_b, held, lane);
+        held_b = first.b;
+        held = 0;
       }
+      held += __popc(m);
+      continue;
+    }
+    Cursor c = first;
+    if (t0 >= c.e && t0 < q.N) c = cursor_at(q, t0);
+    int32_t pos = t0;
+    const int32_t end = min(t0 + 16, q.N);
+    while (pos < end) {
+      const int32_t stop = max(min(c.e, end), pos + 1);   // a bad cu still moves on
+      const uint32_t n = __popc((m >> (pos - t0)) & ((1u << (stop - pos)) - 1u));
+      if (n && c.b >= 0 && c.b < q.S) atomicAdd(a.count + c.b, n);
+      pos = stop;
+      if (pos < end) c = cursor_after(q, c, pos);
     }
   }
+  policy_count_flush(a, held_b, held, lane);
 }
 
-// What a row's tokens share where one sequence holds them all: as loaded, for the
-// row after the one at hand.
-struct PolicyLook {
-  Cursor c;
-  float adv;
-  int32_t n;
-};
-__device__ __forceinline__ void policy_look(const PolicyArgs& a, const Cursor& c, PolicyLook& l) {
-  const int32_t b = min(max(c.b, 0), a.seq.S - 1);
-  l.c = c;
-  if (!a.adv_per_token) l.adv = __ldg(a.adv + b);
-  if (a.reduction == KD_REDUCE_SEQUENCE)
-    l.n = a.mask ? static_cast<int32_t>(__ldcg(a.count + b)) : c.e - seq_begin(a.seq, b);
+// Advantage (where it is the sequence's) and weight of the tokens of sequence b.
+__device__ __forceinline__ void policy_look(const PolicyArgs& a, int32_t b, float seqs, float& adv,
+                                            float& w) {
+  const SeqLayout& q = a.seq;
+  b = min(max(b, 0), q.S - 1);
+  if (!a.adv_per_token) adv = __ldg(a.adv + b);
+  if (a.reduction == KD_REDUCE_SEQUENCE) {
+    const int32_t n = a.mask ? static_cast<int32_t>(__ldcg(a.count + b))
+                             : seq_begin(q, b + 1) - seq_begin(q, b);
+    // at least 1: the weight of a token that does not count is multiplied, too
+    w = 1.f / (seqs * static_cast<float>(max(n, 1)));
+  }
 }
 
 constexpr int POLICY_DEPTH = 2;
@@ -347,7 +409,7 @@ __device__ __forceinline__ uint32_t policy_mask(const PolicyArgs& a, int32_t row
                                                 int32_t first, int32_t last, int lane) {
   if (row >= n_rows) return 0u;
   const int32_t t = row * 128 + 4 * lane;
-  const uint32_t m = load_mask4(a.mask, t, a.seq.N);
+  const uint32_t m = load_mask4(a.mask, t, a.seq.N, a.mask_vec);
   return a.seq.cu ? inside(m, t, first, last) : m;
 }
 
@@ -358,10 +420,10 @@ __device__ __forceinline__ void policy_fetch(const PolicyArgs& a, const PolicyQu
   if (__any_sync(0xffffffffu, m != 0)) {
     const int32_t t = row * 128 + 4 * lane, left = a.seq.N - t;
     if (left > 0) {
-      rows.copy(slot, 0, a.logp + t, left);
-      if (OLD) rows.copy(slot, 1, a.old_logp + t, left);
-      if (REF) rows.copy(slot, 2, a.ref_logp + t, left);
-      if (a.adv_per_token) rows.copy(slot, 3, a.adv + t, left);
+      rows.copy(slot, 0, a.logp + t, left, a.vec);
+      if (OLD) rows.copy(slot, 1, a.old_logp + t, left, a.vec);
+      if (REF) rows.copy(slot, 2, a.ref_logp + t, left, a.vec);
+      if (a.adv_per_token) rows.copy(slot, 3, a.adv + t, left, a.vec);
     }
   }
   rows.commit();
@@ -430,27 +492,27 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
     queue.wait();
     float out[4] = {0.f, 0.f, 0.f, 0.f};
     if (__any_sync(0xffffffffu, m != 0)) {
-      PolicyLook look{{0, INT_MAX}, 0.f, 1};
-      if (need_seq) policy_look(a, cursor_at_warp(q, row * 128, lane), look);
       float lp[4], od[4], rf[4], at[4], wt[4];
       queue.read(slot, 0, lp);
       if (OLD) queue.read(slot, 1, od);
       if (REF) queue.read(slot, 2, rf);
       if (a.adv_per_token) queue.read(slot, 3, at);
-      if (per_seq) w = 1.f / (seqs * static_cast<float>(max(look.n, 1)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        wt[j] = w;
-        if (!a.adv_per_token) at[j] = look.adv;
-      }
-      if (need_seq && look.c.e < row * 128 + 128) {     // a sequence ends in the row
-        PolicyLook l = look;
+      for (int j = 0; j < 4; ++j) wt[j] = w;
+      if (need_seq) {
+        const Cursor c = cursor_at_warp(q, row * 128, lane);
+        if (c.e >= row * 128 + 128) {          // one sequence holds the row
+          policy_look(a, c.b, seqs, at[0], wt[0]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (t0 + j >= l.c.e && t0 + j < q.N) policy_look(a, cursor_at(q, t0 + j), l);
-          if (!a.adv_per_token) at[j] = l.adv;
-          // at least 1: the weight of a token that does not count is multiplied, too
-          if (per_seq) wt[j] = 1.f / (seqs * static_cast<float>(max(l.n, 1)));
+          for (int j = 1; j < 4; ++j) {
+            if (!a.adv_per_token) at[j] = at[0];
+            wt[j] = wt[0];
+          }
+        } else {
+          int32_t b[4];
+          row_sequences(q, c, row * 128, lane, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) policy_look(a, b[j], seqs, at[j], wt[j]);
         }
       }
       // What a token that does not count holds is replaced before it is used: with its A, d and
@@ -513,7 +575,7 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
         held = 0;
       }
     }
-    if (a.dlogp && t0 < q.N) store4(a.dlogp, t0, q.N, out);
+    if (a.dlogp && t0 < q.N) store4(a.dlogp, t0, q.N, out, a.vec);
     policy_fetch<OLD, REF>(a, queue, slot, row + POLICY_DEPTH * n_warps, ahead.m[POLICY_DEPTH - 1],
                            lane);
   }
@@ -592,7 +654,7 @@ policy_main_kernel(const PolicyArgs a) {
 // The whole loss in one block, for batches where launches cost more than the
 // tokens: the counts, then the tokens.
 template <bool OLD, bool REF>
-__global__ void __launch_bounds__(OBJ_THREADS) policy_one_kernel(const PolicyArgs a) {
+__global__ void __launch_bounds__(OBJ_THREADS, 1) policy_one_kernel(const PolicyArgs a) {
   __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PolicyQueue::WARP];
   __shared__ double sm[OBJ_THREADS / 32 * POLICY_STATS];
   __shared__ uint32_t counts[OBJ_THREADS / 32];
@@ -640,10 +702,9 @@ __device__ __forceinline__ void flush_part(SeqPart* to, double sum, uint32_t n, 
   if (lane == 0) *to = SeqPart{sum, static_cast<double>(n)};
 }
 
-// The sequence of token t, where the one before it (c) ends: the next, unless
-// that is empty.
-__device__ __forceinline__ Cursor next_cursor(const SeqLayout& q, const Cursor& c, int32_t t,
-                                              int lane) {
+// The same as cursor_after, by a whole warp.
+__device__ __forceinline__ Cursor cursor_after_warp(const SeqLayout& q, const Cursor& c, int32_t t,
+                                                    int lane) {
   if (c.b + 1 < q.S) {
     const int32_t e = seq_begin(q, c.b + 2);
     if (e > t) return Cursor{c.b + 1, e};
@@ -653,25 +714,55 @@ __device__ __forceinline__ Cursor next_cursor(const SeqLayout& q, const Cursor& 
 
 constexpr int PREF_DEPTH = 4;
 using PrefQueue = RowQueue<2, PREF_DEPTH>;
+constexpr int PREF_SMEM = PrefQueue::WARP + 128;     // bytes of a warp: its rows, a row's mask
 
 __device__ __forceinline__ void pref_fetch(const PrefArgs& a, const PrefQueue& rows, int slot,
                                            int32_t t, int32_t s1, uint32_t m) {
   if (__any_sync(0xffffffffu, m != 0)) {
     if (t < s1) {
-      rows.copy(slot, 0, a.logp + t, s1 - t);
-      if (a.ref_logp) rows.copy(slot, 1, a.ref_logp + t, s1 - t);
+      rows.copy(slot, 0, a.logp + t, s1 - t, a.vec);
+      if (a.ref_logp) rows.copy(slot, 1, a.ref_logp + t, s1 - t, a.vec);
     }
   }
   rows.commit();
 }
 
-__device__ __forceinline__ void pref_sums(const PrefArgs& a, const PrefQueue& queue, int32_t span_i,
+// Sequences [b0, b1), all inside the row [r, r1) that lies in `row` (arrived, mask in
+// `masks`): one lane for each.
+__device__ __forceinline__ void pref_short(const PrefArgs& a, const unsigned char* row,
+                                           const uint8_t* masks, int32_t b0, int32_t b1, int32_t r,
+                                           int32_t r1, int lane) {
+  for (int64_t b = static_cast<int64_t>(b0) + lane; b < b1; b += 32) {
+    const int32_t begin = max(seq_begin(a.seq, static_cast<int32_t>(b)), r);
+    const int32_t end = min(seq_begin(a.seq, static_cast<int32_t>(b) + 1), r1);
+    double sum = 0.0;
+    int n = 0;
+    for (int i = begin - r; i < end - r; ++i) {
+      if (!masks[i]) continue;
+      const float x = reinterpret_cast<const float*>(row)[i];
+      const float y = a.ref_logp ? reinterpret_cast<const float*>(row + 512)[i] : 0.f;
+      sum += static_cast<double>(x) - static_cast<double>(y);
+      ++n;
+    }
+    a.whole[b] = SeqPart{sum, static_cast<double>(n)};
+  }
+}
+
+// smem: PREF_SMEM bytes of this warp.  SHORT: sequences that lie inside a row are taken
+// a lane each, where a row holds several, and not one after the other by the warp.
+// The code for it slows the walk over long ones, so batches choose by their mean
+// length.
+template <bool SHORT>
+__device__ __forceinline__ void pref_sums(const PrefArgs& a, unsigned char* smem, int32_t span_i,
                                           int lane) {
   const SeqLayout& q = a.seq;
+  const PrefQueue queue{smem + 16 * lane};
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + PrefQueue::WARP);
   const int32_t s0 = span_i * a.span, s1 = q.N - s0 < a.span ? q.N : s0 + a.span;
   uint32_t ahead[PREF_DEPTH + 1];            // masks of the next rows
 #pragma unroll
-  for (int k = 0; k <= PREF_DEPTH; ++k) ahead[k] = load_mask4(a.mask, s0 + 128 * k + 4 * lane, s1);
+  for (int k = 0; k <= PREF_DEPTH; ++k)
+    ahead[k] = load_mask4(a.mask, s0 + 128 * k + 4 * lane, s1, a.mask_vec);
 #pragma unroll
   for (int k = 0; k < PREF_DEPTH; ++k)
     pref_fetch(a, queue, k, s0 + 128 * k + 4 * lane, s1, ahead[k]);
@@ -685,7 +776,7 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, const PrefQueue& qu
     const uint32_t m = ahead[0];
 #pragma unroll
     for (int k = 0; k < PREF_DEPTH; ++k) ahead[k] = ahead[k + 1];
-    ahead[PREF_DEPTH] = load_mask4(a.mask, t + 128 * (PREF_DEPTH + 1), s1);
+    ahead[PREF_DEPTH] = load_mask4(a.mask, t + 128 * (PREF_DEPTH + 1), s1, a.mask_vec);
     queue.wait();
     const bool any = __any_sync(0xffffffffu, m != 0);
     float x[4] = {}, y[4] = {};
@@ -699,8 +790,7 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, const PrefQueue& qu
       const double ref = a.ref_logp ? static_cast<double>(y[j]) : 0.0;
       d[j] = mask_byte(m, j) ? static_cast<double>(x[j]) - ref : 0.0;
     }
-    pref_fetch(a, queue, slot, t + 128 * PREF_DEPTH, s1, ahead[PREF_DEPTH - 1]);
-    if (++slot == PREF_DEPTH) slot = 0;
+    if (!SHORT) pref_fetch(a, queue, slot, t + 128 * PREF_DEPTH, s1, ahead[PREF_DEPTH - 1]);
     if (c.e >= r1 && c.b >= 0) {             // the whole row belongs to one sequence
       if (any) {
         sum += (d[0] + d[1]) + (d[2] + d[3]);
@@ -722,9 +812,19 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, const PrefQueue& qu
         if (c.b >= 0) flush_part(begun ? a.whole + c.b : a.head + span_i, sum, n, lane);
         sum = 0.0;
         n = 0;
-        pos = max(stop, pos + 1);            // a bad cu still moves on
-        c = next_cursor(q, c, pos, lane);
         begun = true;
+        pos = max(stop, pos + 1);            // a bad cu still moves on
+        c = cursor_after_warp(q, c, pos, lane);
+        if (SHORT && c.b < q.S && c.e < r1) {    // it ends in the row as well, and others may
+          const Cursor l = cursor_at_warp(q, r1 - 1, lane);
+          masks[lane] = m;
+          __syncwarp();                      // the lanes' copies and masks, for all lanes
+          pref_short(a, smem + slot * PrefQueue::ROW, reinterpret_cast<const uint8_t*>(masks),
+                     max(c.b, 0), min(l.b, q.S), r, r1, lane);
+          __syncwarp();
+          c = l;
+          if (c.b < q.S) pos = max(seq_begin(q, max(c.b, 0)), pos);
+        }
         if (c.b >= q.S) break;               // behind the last sequence
       }
       if (c.b >= q.S) break;
@@ -733,35 +833,77 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, const PrefQueue& qu
       if (c.b >= 0) flush_part(begun ? a.whole + c.b : a.head + span_i, sum, n, lane);
       sum = 0.0;
       n = 0;
-      if (r1 >= s1) return;
-      c = next_cursor(q, c, r1, lane);
+      if (r1 >= s1) break;
+      c = cursor_after_warp(q, c, r1, lane);
       begun = true;
     }
+    // (a row is overwritten after all lanes have read it)
+    if (SHORT) pref_fetch(a, queue, slot, t + 128 * PREF_DEPTH, s1, ahead[PREF_DEPTH - 1]);
+    if (++slot == PREF_DEPTH) slot = 0;
   }
   if (c.b >= 0 && c.b < q.S && c.e > s1)
     flush_part(begun ? a.tail + span_i : a.head + span_i, sum, n, lane);
+  queue.drain();
 }
 
-// Sum and count of sequence b from its parts.  Called by a whole warp.
+// Sum and count of each lane's sequence b (-1: none) from its parts.  Called by a
+// whole warp, which adds the many parts of a long sequence together.
 __device__ __forceinline__ SeqPart pref_join(const PrefArgs& a, int32_t b, int lane) {
-  const int32_t t0 = seq_begin(a.seq, b), t1 = seq_begin(a.seq, b + 1);
-  if (t1 <= t0) return SeqPart{0.0, 0.0};
-  const int32_t i0 = t0 / a.span, i1 = (t1 - 1) / a.span;
-  if (i0 == i1) return SeqPart{__ldcg(&a.whole[b].sum), __ldcg(&a.whole[b].n)};
+  constexpr int ALONE = 4;                   // parts that a lane adds by itself
   SeqPart p{0.0, 0.0};
-  for (int32_t i = i0 + lane; i <= i1; i += 32) {
-    const SeqPart* s = i == i0 ? a.tail + i : a.head + i;
-    p.sum += __ldcg(&s->sum);
-    p.n += __ldcg(&s->n);
+  int32_t i0 = 0, i1 = -1;
+  if (b >= 0) {
+    const int32_t t0 = seq_begin(a.seq, b), t1 = seq_begin(a.seq, b + 1);
+    if (t1 > t0) {
+      i0 = t0 / a.span;
+      i1 = (t1 - 1) / a.span;
+    }
+    if (i1 == i0) {
+      p = SeqPart{__ldcg(&a.whole[b].sum), __ldcg(&a.whole[b].n)};
+    } else if (i1 - i0 < ALONE) {
+      SeqPart part[ALONE];
+#pragma unroll
+      for (int k = 0; k < ALONE; ++k) {
+        part[k] = SeqPart{0.0, 0.0};
+        if (i0 + k > i1) continue;
+        const SeqPart* s = k == 0 ? a.tail + i0 : a.head + i0 + k;
+        part[k] = SeqPart{__ldcg(&s->sum), __ldcg(&s->n)};
+      }
+#pragma unroll
+      for (int k = 0; k < ALONE; ++k) {
+        p.sum += part[k].sum;
+        p.n += part[k].n;
+      }
+    }
   }
-  return SeqPart{warp_sum(p.sum), warp_sum(p.n)};
+  uint32_t many = __ballot_sync(0xffffffffu, i1 - i0 >= ALONE);
+  while (many) {
+    const int src = __ffs(many) - 1;
+    many &= many - 1;
+    const int32_t j0 = __shfl_sync(0xffffffffu, i0, src), j1 = __shfl_sync(0xffffffffu, i1, src);
+    SeqPart part{0.0, 0.0};
+    if (lane == 0) part = SeqPart{__ldcg(&a.tail[j0].sum), __ldcg(&a.tail[j0].n)};
+#pragma unroll 8
+    for (int32_t i = j0 + 1 + lane; i <= j1; i += 32) {
+      const double2 h = __ldcg(reinterpret_cast<const double2*>(a.head + i));
+      part.sum += h.x;
+      part.n += h.y;
+    }
+    part.sum = warp_sum(part.sum);
+    part.n = warp_sum(part.n);
+    if (lane == src) p = part;
+  }
+  return p;
 }
 
-// One warp for each pair: the loss of the pair (returned in every lane), the
-// rewards and the gradient of each of its two sequences' tokens.
+// Pairs from i on, a lane for each of a warp's a.pairs_per_warp: the rewards and the
+// gradient of each of the two sequences' tokens.  Returns the lane's pair's loss.
 __device__ __forceinline__ double pref_pair(const PrefArgs& a, int32_t i, int lane) {
   const int32_t B = a.seq.S / 2;
-  SeqPart c = pref_join(a, i, lane), r = pref_join(a, i + B, lane);
+  const bool mine = lane < a.pairs_per_warp && i + lane < B;
+  i = mine ? i + lane : -1;
+  const SeqPart c = pref_join(a, i, lane), r = pref_join(a, mine ? i + B : -1, lane);
+  if (!mine) return 0.0;
   const double per_c = a.normalize ? 1.0 / fmax(c.n, 1.0) : 1.0;
   const double per_r = a.normalize ? 1.0 / fmax(r.n, 1.0) : 1.0;
   const double sc = c.sum * per_c, sr = r.sum * per_r, D = sc - sr;
@@ -780,13 +922,21 @@ __device__ __forceinline__ double pref_pair(const PrefArgs& a, int32_t i, int la
     if (z != z) loss = z;
     slope = a.beta * (a.smoothing - 1.0 / (1.0 + exp(z)));
   }
-  if (lane == 0) {
-    a.rewards[i] = static_cast<float>(a.beta * sc);
-    a.rewards[i + B] = static_cast<float>(a.beta * sr);
-    a.coef[i] = static_cast<float>(slope * per_c * a.inv_pairs);
-    a.coef[i + B] = static_cast<float>(-slope * per_r * a.inv_pairs);
-  }
+  a.rewards[i] = static_cast<float>(a.beta * sc);
+  a.rewards[i + B] = static_cast<float>(a.beta * sr);
+  a.coef[i] = static_cast<float>(slope * per_c * a.inv_pairs);
+  a.coef[i + B] = static_cast<float>(-slope * per_r * a.inv_pairs);
   return loss;
+}
+
+// This warp's groups of pairs; returns the sum of the lane's losses.
+__device__ __forceinline__ double pref_pairs(const PrefArgs& a, int32_t warp, int32_t n_warps,
+                                             int lane) {
+  const int64_t step = static_cast<int64_t>(n_warps) * a.pairs_per_warp;
+  double sum = 0.0;
+  for (int64_t i = static_cast<int64_t>(warp) * a.pairs_per_warp; i < a.seq.S / 2; i += step)
+    sum += pref_pair(a, static_cast<int32_t>(i), lane);
+  return sum;
 }
 
 // The gradient of rows of 128 tokens, `row` and every n_warps-th after it;
@@ -798,38 +948,34 @@ __device__ __forceinline__ void pref_tokens(const PrefArgs& a, int32_t row, int3
   for (; row < n_rows; row += n_warps) {
     const uint32_t m = m_next;
     const int32_t row0 = row * 128, t0 = row0 + 4 * lane;
-    if (row + n_warps < n_rows) m_next = load_mask4(a.mask, (row + n_warps) * 128 + 4 * lane, q.N);
+    if (row + n_warps < n_rows)
+      m_next = load_mask4(a.mask, (row + n_warps) * 128 + 4 * lane, q.N, a.mask_vec);
     const Cursor c = cursor_at_warp(q, row0, lane);
-    float k = c.b >= 0 && c.b < q.S ? __ldcg(a.coef + c.b) : 0.f;
     float out[4];
     if (c.e >= row0 + 128) {
+      const float k = c.b >= 0 && c.b < q.S ? __ldcg(a.coef + c.b) : 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) out[j] = mask_byte(m, j) ? k : 0.f;
     } else {
-      Cursor l = c;
+      int32_t b[4];
+      row_sequences(q, c, row0, lane, b);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (t0 + j >= l.e && t0 + j < q.N) {
-          l = cursor_at(q, t0 + j);
-          k = l.b >= 0 && l.b < q.S ? __ldcg(a.coef + l.b) : 0.f;
-        }
-        out[j] = mask_byte(m, j) ? k : 0.f;
-      }
+      for (int j = 0; j < 4; ++j)
+        out[j] = mask_byte(m, j) && b[j] >= 0 && b[j] < q.S ? __ldcg(a.coef + b[j]) : 0.f;
     }
-    if (t0 < q.N) store4(a.dlogp, t0, q.N, out);
+    if (t0 < q.N) store4(a.dlogp, t0, q.N, out, a.vec);
   }
 }
 
+template <bool SHORT>
 __global__ void __launch_bounds__(OBJ_THREADS, PREF_BLOCKS_PER_SM)
 pref_sums_kernel(const PrefArgs a) {
-  __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PrefQueue::WARP];
+  __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PREF_SMEM];
   griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
   const int warp = threadIdx.x >> 5;
   const int32_t i = blockIdx.x * (OBJ_THREADS / 32) + warp;
-  const PrefQueue queue{rows + warp * PrefQueue::WARP + 16 * (threadIdx.x & 31)};
-  if (i < a.n_spans) pref_sums(a, queue, i, threadIdx.x & 31);
-  queue.drain();
+  if (i < a.n_spans) pref_sums<SHORT>(a, rows + warp * PREF_SMEM, i, threadIdx.x & 31);
 }
 
 __global__ void __launch_bounds__(OBJ_THREADS) pref_pair_kernel(const PrefArgs a) {
@@ -837,13 +983,8 @@ __global__ void __launch_bounds__(OBJ_THREADS) pref_pair_kernel(const PrefArgs a
   griddep_launch_dependents();
   griddep_wait();                            // the sums
   check_layout(a.seq, a.status);
-  const int lane = threadIdx.x & 31;
-  double v[1] = {0.0};
-  for (int32_t i = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < a.seq.S / 2;
-       i += (gridDim.x * blockDim.x) >> 5) {
-    const double l = pref_pair(a, i, lane);
-    if (lane == 0) v[0] += l;
-  }
+  double v[1] = {pref_pairs(a, (blockIdx.x * OBJ_THREADS + threadIdx.x) >> 5,
+                            (gridDim.x * OBJ_THREADS) >> 5, threadIdx.x & 31)};
   block_sum(v, sm);
   if (threadIdx.x == 0) a.partials[blockIdx.x] = v[0];
 }
@@ -855,7 +996,8 @@ __global__ void __launch_bounds__(OBJ_THREADS) pref_tokens_kernel(const PrefArgs
   __shared__ double sm[OBJ_THREADS / 32];
   const int lane = threadIdx.x & 31;
   const int32_t row = (blockIdx.x * OBJ_THREADS + threadIdx.x) >> 5;
-  const uint32_t m = row < rows_of(a.seq) ? load_mask4(a.mask, row * 128 + 4 * lane, a.seq.N) : 0u;
+  const uint32_t m =
+      row < rows_of(a.seq) ? load_mask4(a.mask, row * 128 + 4 * lane, a.seq.N, a.mask_vec) : 0u;
   griddep_wait();                            // the pairs
   if (a.dlogp) pref_tokens(a, row, (gridDim.x * OBJ_THREADS) >> 5, m, lane);
   if (blockIdx.x != gridDim.x - 1) return;
@@ -867,27 +1009,22 @@ __global__ void __launch_bounds__(OBJ_THREADS) pref_tokens_kernel(const PrefArgs
 
 // The three steps in one block, for batches where launches cost more than the
 // tokens.
-__global__ void __launch_bounds__(OBJ_THREADS) pref_one_kernel(const PrefArgs a) {
-  __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PrefQueue::WARP];
+template <bool SHORT>
+__global__ void __launch_bounds__(OBJ_THREADS, 1) pref_one_kernel(const PrefArgs a) {
+  __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PREF_SMEM];
   __shared__ double sm[OBJ_THREADS / 32];
   constexpr int NW = OBJ_THREADS / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PrefQueue queue{rows + warp * PrefQueue::WARP + 16 * (threadIdx.x & 31)};
   if (threadIdx.x == 0) *a.status = 0u;
-  for (int32_t i = warp; i < a.n_spans; i += NW) {
-    pref_sums(a, queue, i, lane);
-    queue.drain();
-  }
+  for (int32_t i = warp; i < a.n_spans; i += NW)
+    pref_sums<SHORT>(a, rows + warp * PREF_SMEM, i, lane);
   __syncthreads();
   check_layout(a.seq, a.status);
-  double v[1] = {0.0};
-  for (int32_t i = warp; i < a.seq.S / 2; i += NW) {
-    const double l = pref_pair(a, i, lane);
-    if (lane == 0) v[0] += l;
-  }
+  double v[1] = {pref_pairs(a, warp, NW, lane)};
   block_sum(v, sm);                          // its barriers also publish the gradients
   if (threadIdx.x == 0) *a.loss = static_cast<float>(v[0] * a.inv_pairs);
-  if (a.dlogp) pref_tokens(a, warp, NW, load_mask4(a.mask, 4 * threadIdx.x, a.seq.N), lane);
+  if (a.dlogp)
+    pref_tokens(a, warp, NW, load_mask4(a.mask, 4 * threadIdx.x, a.seq.N, a.mask_vec), lane);
 }
 
 // ----------------------------------------------------------------------------
@@ -895,8 +1032,10 @@ __global__ void __launch_bounds__(OBJ_THREADS) pref_one_kernel(const PrefArgs a)
 // ----------------------------------------------------------------------------
 namespace {
 
-// Batches of at most this many tokens (and sequences) run in one block.
-constexpr int64_t ONE_BLOCK_TOKENS = 4096;
+// Batches of at most this many tokens and sequences run in one block.  (512, 4096 and
+// 8192 tokens: policy 5.4, 7.5 and 10.9 us in one block, 10.2 in several; preference
+// 5.2, 8.1 and 12.4 against 7.2, 8.4 and 8.5.)
+constexpr int64_t ONE_BLOCK_TOKENS = 4096, ONE_BLOCK_SEQUENCES = 1024;
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), int64_t blocks, int threads, cudaStream_t s, bool pdl,
@@ -925,7 +1064,7 @@ namespace {
 template <bool OLD, bool REF>
 kd_status policy_launch(PolicyArgs a, cudaStream_t s, int num_sms) {
   const SeqLayout& q = a.seq;
-  if (q.N <= ONE_BLOCK_TOKENS && q.S <= ONE_BLOCK_TOKENS)
+  if (q.N <= ONE_BLOCK_TOKENS && q.S <= ONE_BLOCK_SEQUENCES)
     return launch(policy_one_kernel<OLD, REF>, 1, OBJ_THREADS, s, false, a) == cudaSuccess
                ? KD_OK
                : KD_ERR_CUDA;
@@ -964,16 +1103,26 @@ kd_status policy_loss(const PolicyArgs& a, cudaStream_t s, int num_sms) {
                     : policy_launch<false, false>(a, s, num_sms);
 }
 
-kd_status preference_loss(const PrefArgs& a, cudaStream_t s, int num_sms) {
+kd_status preference_loss(PrefArgs a, cudaStream_t s, int num_sms) {
   const SeqLayout& q = a.seq;
-  if (q.N <= ONE_BLOCK_TOKENS && q.S <= ONE_BLOCK_TOKENS)
-    return launch(pref_one_kernel, 1, OBJ_THREADS, s, false, a) == cudaSuccess ? KD_OK
-                                                                                    : KD_ERR_CUDA;
   constexpr int W = OBJ_THREADS / 32;
-  if (launch(pref_sums_kernel, (a.n_spans + W - 1) / W, OBJ_THREADS, s, false, a) != cudaSuccess)
+  // a warp for each pair as long as they last, then a lane
+  const bool one = q.N <= ONE_BLOCK_TOKENS && q.S <= ONE_BLOCK_SEQUENCES;
+  const int64_t pairs = q.S / 2, warps = one ? W : static_cast<int64_t>(W) * 4 * num_sms;
+  a.pairs_per_warp = static_cast<int32_t>(at_most((pairs + warps - 1) / warps, 32));
+  // (2048 sequences of 8 tokens: 9 us with a lane each, 12 without; of 30: 10.4 and 10.3)
+  const bool few_tokens = static_cast<int64_t>(q.N) < static_cast<int64_t>(PREF_SHORT_MEAN) * q.S;
+  if (one)
+    return launch(few_tokens ? pref_one_kernel<true> : pref_one_kernel<false>, 1, OBJ_THREADS, s,
+                  false, a) == cudaSuccess
+               ? KD_OK
+               : KD_ERR_CUDA;
+  if (launch(few_tokens ? pref_sums_kernel<true> : pref_sums_kernel<false>,
+             (a.n_spans + W - 1) / W, OBJ_THREADS, s, false, a) != cudaSuccess)
     return KD_ERR_CUDA;
   const int64_t cap = at_most(8 * num_sms, OBJ_MAX_BLOCKS);
-  const int64_t pair_blocks = at_most((q.S / 2 + W - 1) / W, cap);
+  const int64_t groups = (pairs + a.pairs_per_warp - 1) / a.pairs_per_warp;
+  const int64_t pair_blocks = at_most((groups + W - 1) / W, cap);
   if (launch(pref_pair_kernel, pair_blocks, OBJ_THREADS, s, true, a) != cudaSuccess)
     return KD_ERR_CUDA;
   const int64_t per_block = 4 * OBJ_THREADS;

@@ -25,6 +25,7 @@ import os
 import re
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG_DIR, "libkd.so")
@@ -630,6 +631,7 @@ class HeadLogprobs(torch.autograd.Function):
         return logp
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         h, W, targets, lse = ctx.saved_tensors
         # dW leaves the kernel in W's type where it is formed in one go, and is added up in fp32
@@ -723,6 +725,7 @@ class PolicyLoss(torch.autograd.Function):
         return loss, stats
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, _):
         (dlogp,) = ctx.saved_tensors
         return dlogp * g, None, None, None
@@ -778,6 +781,7 @@ class PreferenceLoss(torch.autograd.Function):
         return loss, rewards
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, _):
         (dlogp,) = ctx.saved_tensors
         return dlogp * g, None

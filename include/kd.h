@@ -25,6 +25,9 @@
  *     status word of its workspace when it starts.
  *   - A workspace may not be used by two calls that can run at the same time.
  *   - Device pointers must be 16-byte aligned; `ws` must be 1024-byte aligned.
+ *     (Arrays over tokens or positions of the post-training entry points, and
+ *     their sequences' ones, need only the alignment of their elements: slices
+ *     of a batch will do.)
  *   - Inside one call, consecutive kernels use programmatic dependent launch:
  *     a kernel may start while the one before it finishes, and waits inside
  *     for that kernel's results.  The first kernel of every call is launched

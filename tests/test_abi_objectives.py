@@ -32,8 +32,8 @@ def _head(call, **kw):
 @pytest.mark.parametrize("call", ["fwd", "bwd"])
 def test_head_logprob_refusals(call):
     for kw in (dict(h=None), dict(W=None), dict(targets=None), dict(T=0), dict(chunk=0), dict(tau=0.0), dict(V=0),
-               dict(tau=math.nan), dict(h=FAKE + 8), dict(targets=FAKE + 4), dict(ws=None), dict(ws=FAKE + 256),
-               dict(lse=None), dict(lse=FAKE + 4)):
+               dict(tau=math.nan), dict(h=FAKE + 8), dict(targets=FAKE + 2), dict(ws=None), dict(ws=FAKE + 256),
+               dict(lse=None), dict(lse=FAKE + 2)):
         assert _head(call, **kw) == kd.KD_ERR_INVALID_ARG, kw
     for kw in (dict(dtype=7), dict(d=12), dict(V=2 ** 31), dict(T=1 << 40), dict(T=1 << 31, chunk=1 << 31)):
         assert _head(call, **kw) == kd.KD_ERR_UNSUPPORTED, kw
@@ -71,8 +71,8 @@ def _policy(**kw):
 
 def test_policy_refusals():
     for kw in (dict(logp=None), dict(adv=None), dict(loss=None), dict(stats=None), dict(ws=None),
-               dict(logp=FAKE + 4), dict(old=FAKE + 8), dict(ref=FAKE + 4), dict(mask=FAKE + 1), dict(g=FAKE + 4),
-               dict(per=1, adv=FAKE + 4), dict(adv=FAKE + 2), dict(ws=FAKE + 512), dict(cu=FAKE + 2),
+               dict(logp=FAKE + 2), dict(old=FAKE + 1), dict(ref=FAKE + 2), dict(g=FAKE + 3),
+               dict(per=1, adv=FAKE + 2), dict(adv=FAKE + 2), dict(ws=FAKE + 512), dict(cu=FAKE + 2),
                dict(S=0), dict(N=0), dict(S=-1), dict(N=65), dict(lo=-0.1), dict(lo=1.5), dict(lo=math.nan),
                dict(hi=-0.1), dict(hi=math.nan), dict(kl=math.nan), dict(kl=math.inf), dict(kl=0.1, ref=None),
                dict(red=3), dict(red=-1), dict(red=2), dict(red=2, denom=-1.0), dict(red=2, denom=math.inf)):
@@ -80,6 +80,8 @@ def test_policy_refusals():
     for kw in (dict(N=2 ** 31), dict(N=2 ** 31 - 1023, cu=FAKE), dict(S=2 ** 31, cu=FAKE)):
         assert _policy(**kw) == kd.KD_ERR_UNSUPPORTED, kw
     assert _policy(ws_bytes=1024) == kd.KD_ERR_WORKSPACE
+    # slices of a batch: the elements' alignment is enough
+    assert _policy(ws_bytes=1024, logp=FAKE + 4, old=FAKE + 8, mask=FAKE + 1, adv=FAKE + 4, g=FAKE + 12) == kd.KD_ERR_WORKSPACE
     assert kd.kd_policy_loss_workspace_size(0, 5) == 0 == kd.kd_policy_loss_workspace_size(5, 2 ** 31)
 
 
@@ -93,8 +95,8 @@ def _pref(**kw):
 
 
 def test_preference_refusals():
-    for kw in (dict(logp=None), dict(loss=None), dict(rew=None), dict(ws=None), dict(logp=FAKE + 4),
-               dict(ref=FAKE + 4), dict(mask=FAKE + 2), dict(g=FAKE + 8), dict(cu=FAKE + 1), dict(B=0), dict(N=0),
+    for kw in (dict(logp=None), dict(loss=None), dict(rew=None), dict(ws=None), dict(logp=FAKE + 2),
+               dict(ref=FAKE + 1), dict(g=FAKE + 2), dict(cu=FAKE + 1), dict(B=0), dict(N=0),
                dict(N=65), dict(kind=3), dict(kind=-1), dict(beta=0.0), dict(beta=-1.0), dict(beta=math.inf),
                dict(margin=math.nan), dict(eps=0.5), dict(eps=-0.1), dict(kind=2, margin=0.5), dict(kind=1, eps=0.1),
                dict(kind=2, eps=0.1), dict(total=3)):
@@ -102,6 +104,7 @@ def test_preference_refusals():
     for kw in (dict(N=2 ** 31), dict(B=2 ** 30, total=2 ** 30, cu=FAKE)):
         assert _pref(**kw) == kd.KD_ERR_UNSUPPORTED, kw
     assert _pref(ws_bytes=1024) == kd.KD_ERR_WORKSPACE
+    assert _pref(ws_bytes=1024, logp=FAKE + 4, ref=FAKE + 8, mask=FAKE + 3, g=FAKE + 4) == kd.KD_ERR_WORKSPACE
     assert kd.kd_preference_loss_workspace_size(0, 5) == 0 == kd.kd_preference_loss_workspace_size(2 ** 30, 5)
 
 

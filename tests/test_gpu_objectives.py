@@ -37,6 +37,11 @@ LAYOUTS = {
     "packed-all-empty": ([0, 0], 7, 3),
     "packed-long": ([1, 20000, 0, 3, 2, 1, 9000, 64, 0, 130], 3, 4097),
     "packed-many-short": (list(range(9)) * 700, 0, 2),
+    "rows-of-1-2048": (2048, 1),
+    "rows-of-7": (900, 7),
+    "packed-short": ([(k * 7) % 4 for k in range(1501)] + [2], 1, 1),
+    "packed-short-among-long": ([1, 2, 0, 3, 500, 1, 1, 1, 0, 0, 2, 700] * 30, 2, 3),
+    "packed-many-empty": ([0] * 700 + [5] + [0] * 2000 + [9000, 0, 0, 1] * 2, 0, 0),
     "packed-128s": ([128, 256, 0, 128, 384, 128] * 30, 128, 0),
 }
 
@@ -315,3 +320,76 @@ def test_two_captured_graphs_and_another_stream(name):
             side.synchronize()
             for a, b in zip(again, want):
                 assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+@pytest.mark.parametrize("name", ["rows-of-129", "rows-of-1000", "packed-small", "packed-long"])
+def test_slices_of_a_batch(name, shift):
+    """Arrays that begin at any element of a buffer: the same bits as aligned ones,
+    and nothing around the gradient is written."""
+    require_gpu()
+    x = _make(name, 14, True)
+
+    def moved(t):
+        buf = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+        view = buf[shift:shift + t.numel()].view(t.shape)
+        return view.copy_(t)
+
+    y = {k: moved(x[k]) for k in ("logp", "old", "ref", "mask", "adv", "adv_tok")}
+    cu = None if x["cu"] is None else moved(x["cu"])
+    for per in ("sequence", "token"):
+        a, b = (z["adv"] if per == "sequence" else z["adv_tok"] for z in (x, y))
+        kw = dict(kl_coef=0.1, reduction="sequence", advantages_per=per)
+        want = kd.policy_loss(x["logp"], x["old"], a, mask=x["mask"], ref_logp=x["ref"], cu_seqlens=x["cu"], **kw)
+        got = kd.policy_loss(y["logp"], y["old"], b, mask=y["mask"], ref_logp=y["ref"], cu_seqlens=cu, **kw)
+        assert all(torch.equal(p, q) for p, q in zip(want, got))
+    want = kd.preference_loss(x["logp"], ref_logp=x["ref"], mask=x["mask"], cu_seqlens=x["cu"])
+    got = kd.preference_loss(y["logp"], ref_logp=y["ref"], mask=y["mask"], cu_seqlens=cu)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    # the gradient into a place of the caller's, by the raw call
+    n, S = x["N"], x["S"]
+    out = torch.full((n + 16,), 7.0, device="cuda")
+    ws = kd.alloc_workspace(kd.kd_preference_loss_workspace_size(S // 2, n), "cuda")
+    small = torch.empty(S + 1, device="cuda")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    assert kd.kd_preference_loss(p(x["logp"]), p(x["ref"]), p(x["mask"]), p(x["cu"]), S // 2, n, 0, 0.1, 0.0, 0.0, 0,
+                                 S // 2, small.data_ptr(), small.data_ptr() + 4, out.data_ptr() + 4 * (shift + 4),
+                                 ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == kd.KD_OK
+    assert torch.equal(out[shift + 4:shift + 4 + n], want[2].reshape(-1))
+    assert bool((out[:shift + 4] == 7).all()) and bool((out[shift + 4 + n:] == 7).all())
+
+
+def test_offsets_past_32_bits():
+    """2^30 + 640 tokens: byte offsets pass 2^32."""
+    require_gpu()
+    S, L = 4, (1 << 28) + 160
+    n = S * L
+    logp = torch.full((S, L), -1.0, device="cuda")
+    logp[3, -1] = -0.75
+    old = torch.full((S, L), -1.0, device="cuda")
+    adv = torch.tensor([1.0, 1.0, 1.0, 2.0], device="cuda")
+    loss, stats, g = kd.policy_loss(logp, old, adv, clip_high=0.5)
+    assert stats[0].item() == float(np.float32(n))
+    assert loss.item() == pytest.approx(-1.25, rel=1e-6)
+    assert g[0, 0].item() == pytest.approx(-1 / n, rel=1e-6) and g[2, -1].item() == pytest.approx(-1 / n, rel=1e-6)
+    assert g[3, -1].item() == pytest.approx(-2 * np.exp(0.25) / n, rel=1e-6)
+    del old
+    loss, rewards, g = kd.preference_loss(logp, beta=1e-6)
+    assert rewards[2].item() == pytest.approx(-L * 1e-6, rel=1e-6)
+    assert rewards[3].item() == pytest.approx((-L + 0.25) * 1e-6, rel=1e-6)
+    # pairs (0, 2) with D = 0 and (1, 3) with D = -1/4: beta sigmoid(-beta D) / 2 for each rejected token
+    assert g[2, 0].item() == pytest.approx(1e-6 * 0.5 / 2, rel=1e-6)
+    assert g[3, -1].item() == g[3, 0].item() == pytest.approx(1e-6 / (1 + np.exp(-0.25e-6)) / 2, rel=1e-6)
+
+
+@pytest.mark.parametrize("S,L", [(2, 3), (2, 5000), (2048, 9)])
+def test_a_batch_that_the_mask_leaves_empty(S, L):
+    require_gpu()
+    x = torch.full((S, L), float("nan"), device="cuda")
+    mask = torch.zeros((S, L), dtype=torch.uint8, device="cuda")
+    adv = torch.full((S,), float("nan"), device="cuda")
+    for reduction in ("token", "sequence"):
+        loss, stats, g = kd.policy_loss(x, x, adv, mask=mask, ref_logp=x, kl_coef=0.1, reduction=reduction)
+        assert loss.item() == 0 and stats.tolist() == [0, 0, 0, 0] and bool((g == 0).all())
+    loss, rewards, g = kd.preference_loss(x, mask=mask, length_normalize=True)
+    assert loss.item() == pytest.approx(np.log(2), rel=1e-6) and bool((rewards == 0).all()) and bool((g == 0).all())

@@ -90,8 +90,8 @@ def test_micro_batches_add_up():
     dW, loss = None, 0.0
     for k in (0, 3):
         rows = slice(37 * k, 37 * (k + 3))
-        part = posttrain.policy_step(h[rows].clone(), W, tgt[k:k + 3].clone(), old[k:k + 3].clone(), adv[k:k + 3],
-                                     chunk=64, reduction="fixed", denom=n, dW=dW, accumulate_dW=dW is not None)
+        part = posttrain.policy_step(h[rows], W, tgt[k:k + 3], old[k:k + 3], adv[k:k + 3], chunk=64,
+                                     reduction="fixed", denom=n, dW=dW, accumulate_dW=dW is not None)
         dW, loss = part.dW, loss + part.loss.item()
         # the weights 1 / n differ by a rounding, which may move dz across one of bf16's
         assert bool(((part.dH.double() - whole.dH[rows].double()).abs()
