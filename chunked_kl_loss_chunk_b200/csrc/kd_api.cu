@@ -272,12 +272,22 @@ static int64_t head_fwd_chunk(int64_t chunk) {
   return chunk > kd::KD_HEAD_FWD_ROWS ? chunk : kd::KD_HEAD_FWD_ROWS;
 }
 
+// Whether the backward forms dz of all T rows at once.
+static bool one_group(int64_t T, int64_t chunk) {
+  return (T + kd::KD_DW_GROUP - 1) / kd::KD_DW_GROUP <= chunk;
+}
+
 size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int dtype,
-                                      int backward) {
+                                      int use) {
   if (T < 1 || d < 1 || V < 1 || chunk < 1) return 0;
+  if (use == KD_HEAD_KEEP) {
+    if (!one_group(T, chunk)) return 0;
+    const kd::KeepLayout K = kd::keep_layout(T, d, V, chunk, head_fwd_chunk(chunk), dtype);
+    return K.ok ? K.total : 0;
+  }
   const kd::WsLayout F = kd::ws_layout(T, d, V, 1, head_fwd_chunk(chunk), dtype);
   if (!F.ok) return 0;
-  if (!backward) return F.fwd_end;
+  if (use == KD_HEAD_FWD) return F.fwd_end;
   const kd::WsLayout L = kd::ws_layout(T, d, V, 1, chunk, dtype);
   if (!L.ok) return 0;
   return L.total > F.fwd_end ? L.total : F.fwd_end;
@@ -286,7 +296,7 @@ size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t c
 // Checks shared by the two calls below.
 static kd_status validate_head(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                                int64_t V, const int32_t* targets, int64_t chunk, float tau,
-                               void* ws, size_t ws_bytes, bool backward) {
+                               void* ws, size_t ws_bytes, bool backward, bool keep) {
   if (!targets || !aligned(targets, 4)) return KD_ERR_INVALID_ARG;
   // the head's own checks, with h in the places of the two arrays of a cache with K = 1
   const kd_status st =
@@ -294,6 +304,11 @@ static kd_status validate_head(const void* h, const void* W, int dtype, int64_t 
                                static_cast<const int32_t*>(h), 1, chunk, tau);
   if (st != KD_OK) return st;
   if (!ws || !aligned(ws, kd::KD_WS_ALIGN)) return KD_ERR_INVALID_ARG;
+  if (keep) {
+    if (!one_group(T, chunk)) return KD_ERR_UNSUPPORTED;
+    const kd::KeepLayout K = kd::keep_layout(T, d, V, chunk, head_fwd_chunk(chunk), dtype);
+    return K.ok && ws_bytes >= K.total ? KD_OK : KD_ERR_WORKSPACE;
+  }
   const kd::WsLayout L =
       kd::ws_layout(T, d, V, 1, backward ? chunk : head_fwd_chunk(chunk), dtype);
   if (!L.ok || ws_bytes < (backward ? L.total : L.fwd_end)) return KD_ERR_WORKSPACE;
@@ -302,40 +317,44 @@ static kd_status validate_head(const void* h, const void* W, int dtype, int64_t 
 
 kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
-                              float* logp, float* lse, void* ws, size_t ws_bytes, void* stream) {
+                              int keep, float* logp, float* lse, void* ws, size_t ws_bytes,
+                              void* stream) {
   const kd_status st = validate_head(h, W, dtype, T, d, V, targets, chunk, temperature, ws,
-                                     ws_bytes, false);
+                                     ws_bytes, false, keep != 0);
   if (st != KD_OK) return st;
   if (!logp || !lse || !aligned(logp, 4) || !aligned(lse, 4)) return KD_ERR_INVALID_ARG;
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
   kd::RowTerms rt;
   rt.targets = targets;
+  rt.keep_chunk = keep ? chunk : 0;
   return kd::fused_fwd(h, W, dtype, T, 1, d, V, rt, head_fwd_chunk(chunk), temperature, nullptr,
                        lse, logp, ws, static_cast<cudaStream_t>(stream), sms, kd::wait_limit_ns());
 }
 
 kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
-                              const float* lse, const float* grad_logp, const float* grad_loss,
-                              void* dH, void* dW, int dW_dtype, int accumulate_dW, void* ws,
+                              const float* lse, const float* kept_logp, const float* grad_logp,
+                              const float* grad_loss, void* dH, void* dW, int dW_dtype, int accumulate_dW, void* ws,
                               size_t ws_bytes, void* stream) {
   const kd_status st = validate_head(h, W, dtype, T, d, V, targets, chunk, temperature, ws,
-                                     ws_bytes, true);
+                                     ws_bytes, true, kept_logp != nullptr);
   if (st != KD_OK) return st;
   if (!lse || !grad_logp || (!dH && !dW)) return KD_ERR_INVALID_ARG;
-  if (!aligned(lse, 4) || !aligned(grad_logp, 4) || !aligned(dH, 16) || !aligned(dW, 16) ||
+  if (!aligned(lse, 4) || !aligned(kept_logp, 4) || !aligned(grad_logp, 4) || !aligned(dH, 16) || !aligned(dW, 16) ||
       !aligned(grad_loss, 4))
     return KD_ERR_INVALID_ARG;
   if (dW && dW_dtype != KD_DTYPE_F32 &&
       (dW_dtype != KD_DTYPE_BF16 || dtype != KD_DTYPE_BF16 || accumulate_dW ||
-       (T + kd::KD_DW_GROUP - 1) / kd::KD_DW_GROUP > chunk))
+       !one_group(T, chunk)))
     return KD_ERR_UNSUPPORTED;
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
   kd::RowTerms rt;
   rt.targets = targets;
   rt.grad_rows = grad_logp;
+  rt.kept_logp = kept_logp;
+  rt.keep_chunk = kept_logp ? head_fwd_chunk(chunk) : 0;
   return kd::fused_bwd(h, W, dtype, T, 1, d, V, rt, chunk, temperature, lse, grad_loss, dH, dW,
                        dW ? dW_dtype : KD_DTYPE_F32, accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
                        kd::wait_limit_ns());

@@ -50,7 +50,8 @@ enum EpiKind : int {
   EPI_BWD_DZ = 1,         // dz boxes
   EPI_STORE_W = 2,        // dW boxes in the operands' dtype, stored
   EPI_ACCUM_W = 3,        // fp32 dW boxes, stored or added
-  EPI_STORE_PARTIAL = 4   // fp32 boxes of one K-split's partial dH
+  EPI_STORE_PARTIAL = 4,  // fp32 boxes of one K-split's partial dH
+  EPI_FWD_KEEP = 5        // EPI_FWD_LSE, and its exponentials stored for the backward
 };
 
 struct GemmArgs {
@@ -65,6 +66,8 @@ struct GemmArgs {
   const int32_t* idx_sorted;  // [T, Ktop], ascending per row
   const float* p_sorted;      // [T, Ktop]
   const float2* row_stats;    // [T]: (S = sum p, sum p log p)
+  float* block_max;           // EPI_FWD_KEEP: [blocks of 32 columns][ld_max], reference of each
+  int64_t ld_max;             //   stored exponential
   float4* partials;           // fwd: [M, n_tiles] (max z, sum exp2((z-max) zscale), gather, -)
   const float* lse;           // bwd: [T]
   const float* grad_loss;     // bwd: device scalar or null (1)
@@ -161,7 +164,7 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
   const int n0 = nb * BN;
   const int y_box = y_extra + m_base + quad * 32;  // first output row of this warp's boxes
 
-  if constexpr (EPI == EPI_FWD_LSE || EPI == EPI_BWD_DZ) {
+  if constexpr (EPI == EPI_FWD_LSE || EPI == EPI_FWD_KEEP || EPI == EPI_BWD_DZ) {
     const int64_t t = g.row0 + m;         // global position
     const int32_t* ids = g.idx_sorted + t * g.Ktop;
     const float* ps = g.p_sorted + t * g.Ktop;
@@ -171,7 +174,7 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
     float np = ptr < g.Ktop ? __ldg(ps + ptr) : 0.f;
     const float zs = g.zscale;
 
-    if constexpr (EPI == EPI_FWD_LSE) {
+    if constexpr (EPI == EPI_FWD_LSE || EPI == EPI_FWD_KEEP) {
       float run_m = -INFINITY, run_s = 0.f, gat = 0.f;
 #pragma unroll 1
       for (int c = 0; c < BN / 32; ++c) {
@@ -204,9 +207,27 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
           const float off = -nm * zs;
           float s = 0.f;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s += ex2_approx(fmaf(v[j], zs, off));
+          for (int j = 0; j < 32; ++j) {
+            const float e = ex2_approx(fmaf(v[j], zs, off));
+            if constexpr (EPI == EPI_FWD_KEEP) v[j] = e;
+            s += e;
+          }
           run_s = run_s * ex2_approx((run_m - nm) * zs) + s;
           run_m = nm;
+        }
+        if constexpr (EPI == EPI_FWD_KEEP) {
+          // exp((z - nm) / tau), rounded once to the operands' type, and its nm; a row of
+          // nothing but -inf keeps zeros
+          if (nm == -INFINITY) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          if (row_ok) g.block_max[static_cast<int64_t>(base / 32) * g.ld_max + t] = nm;
+          unsigned char* box = boxes + (c & 1) * EPI_BUF_BYTES;
+          box_reuse_wait();
+          if constexpr (sizeof(Elem) == 4) stage_box_f32(box, lane, v);
+          else stage_box_bf16(box, lane, v);
+          emit_box<Elem>(tmC, box, base, y_box, false);
         }
       }
       // every cached index inside this tile's columns was gathered

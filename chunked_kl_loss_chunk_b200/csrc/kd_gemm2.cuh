@@ -194,7 +194,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
-    if (EPI != EPI_FWD_LSE) tma_prefetch_desc(&tmC);
+    if (EPI != EPI_FWD_LSE) tma_prefetch_desc(&tmC);     // the one kind without an output box
   }
   if (warp == 1) {
     tmem_alloc2(tmem_slot, TMEM_COLS);

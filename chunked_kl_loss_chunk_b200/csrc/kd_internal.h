@@ -41,6 +41,16 @@ struct WsLayout {
 
 WsLayout ws_layout(int64_t T, int64_t d, int64_t V, int K, int64_t chunk, int dtype);
 
+// Workspace of a head log-probability forward that keeps its exponentials for the
+// backward: ws_layout(T, d, V, 1, chunk), whose dz they lie in, then the forward's
+// partials (of fwd_chunk rows) and the reference of each block of 32 exponentials.
+struct KeepLayout {
+  size_t part = 0, block_max = 0, total = 0;
+  int64_t ld_max = 0;
+  bool ok = true;
+};
+KeepLayout keep_layout(int64_t T, int64_t d, int64_t V, int64_t chunk, int64_t fwd_chunk, int dtype);
+
 // Host validation shared by every fused-loss entry point, for everything but
 // the workspace and the outputs: non-null, 16-byte-aligned inputs; positive
 // sizes with K <= V; a finite tau > 0 (KD_ERR_INVALID_ARG); a supported dtype,
@@ -60,6 +70,11 @@ struct RowTerms {
   uint32_t flags = 0;
   const int32_t* targets = nullptr;
   const float* grad_rows = nullptr;
+  // The forward keeps its exponentials (T <= KD_DW_GROUP of the backward's chunk, which
+  // keep_chunk then is); the backward makes dz of them when kept_logp, the forward's logp,
+  // is given (keep_chunk is then the forward's chunk).
+  int64_t keep_chunk = 0;
+  const float* kept_logp = nullptr;
 };
 
 // The fused loss over T positions whose loss and gradients are normalised by

@@ -335,6 +335,80 @@ combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64
   }
 }
 
+// dz from the exponentials that EPI_FWD_KEEP left, in place: with the block's
+// reference m, coef S exp(a - LSE) = (coef S 2^(m zscale - LSE log2 e)) kept.  The
+// target's entry does not come from the rounded exponential (1 - p would lose its
+// digits where p is near 1) but from logp: coef p (e^logp - 1), p = S = -g.
+// Elementwise over T x V: a pass of the memory (0.17 ms at 2048 x 131072) in the
+// place of a product (1.6 ms).  A block takes 32 rows x 32 vectors of 16 bytes.
+constexpr int KEPT_ROWS = 32;
+template <typename Elem>
+__global__ void __launch_bounds__(256)
+kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float zscale, float inv_tau,
+               const float* __restrict__ block_max, int64_t ld_max, const float* __restrict__ lse,
+               const float* __restrict__ logp, const float* __restrict__ grad_loss,
+               const int32_t* __restrict__ target, const float2* __restrict__ stats) {
+  constexpr int VEC = 16 / sizeof(Elem), COLS = 32 * VEC, BLOCKS = COLS / 32;
+  __shared__ float scale[KEPT_ROWS][BLOCKS];
+  griddep_launch_dependents();
+  griddep_wait();                       // the prepared rows
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * KEPT_ROWS;
+  const float coef = (grad_loss ? __ldg(grad_loss) : 1.f) * inv_tau;
+  for (int64_t col0 = static_cast<int64_t>(blockIdx.y) * COLS; col0 < V;
+       col0 += static_cast<int64_t>(gridDim.y) * COLS) {
+    if (warp < BLOCKS) {
+      const int64_t t = row0 + lane, block = col0 / 32 + warp;
+      float k = 0.f;
+      if (t < T && block * 32 < V) {
+        const float S = stats[t].x, m = block_max[block * ld_max + t];
+        if (S != 0.f && m != -INFINITY)
+          k = coef * S * ex2_approx(fmaf(m, zscale, -lse[t] * 1.4426950408889634f));
+      }
+      scale[lane][warp] = k;
+    }
+    __syncthreads();
+    const int64_t col = col0 + lane * VEC;
+#pragma unroll
+    for (int i = 0; i < KEPT_ROWS / 8; ++i) {
+      const int r = warp * (KEPT_ROWS / 8) + i;
+      const int64_t t = row0 + r;
+      if (t >= T || col >= V) continue;      // the row's pitch holds its last vector whole
+      const float k = scale[r][lane * VEC / 32];
+      uint4* at = reinterpret_cast<uint4*>(dz + t * ldz + col);
+      const uint4 q = *at;
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      float x[VEC];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(Elem) == 4) {
+          x[j] = __uint_as_float(w[j]) * k;
+        } else {
+          x[2 * j] = __uint_as_float(w[j] << 16) * k;
+          x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * k;
+        }
+      }
+      const int64_t y = static_cast<int64_t>(target[t]) - col;   // INT32_MAX: no target
+      if (y >= 0 && y < VEC) {
+        const float v = coef * stats[t].x * expm1f(logp[t]);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (j == y) x[j] = v;
+      }
+      uint4 out;
+      if constexpr (sizeof(Elem) == 4) {
+        out = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                         __float_as_uint(x[3]));
+      } else {
+        out = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                         pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      }
+      *at = out;
+    }
+    __syncthreads();
+  }
+}
+
 // dH rows of a chunk = sum over K-splits of the fp32 partials, in split order.
 // One thread per 4 consecutive elements (d % 8 == 0), grid-stride over a grid
 // small enough to be resident at once (so that the next kernel can launch
@@ -458,10 +532,10 @@ bool make_out_map(CUtensorMap* map, const void* base, bool f32, uint64_t inner, 
 // Launches a small kernel with programmatic stream serialization (it may start
 // while the kernel before it runs, and waits inside for that kernel's results).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned block, cudaStream_t s,
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, unsigned block, cudaStream_t s,
                        Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = s;
@@ -538,8 +612,8 @@ int max_pair_clusters(Kern kern, int num_sms) {
 template <typename Elem, int A_MN, int B_MN, int EPI>
 cudaError_t launch_gemm2(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                          GemmArgs g, cudaStream_t s, int num_sms) {
-  static constexpr int kKind[5] = {KD_GEMM_FWD_LSE, KD_GEMM_BWD_DZ, KD_GEMM_DW, KD_GEMM_DW,
-                                   KD_GEMM_DH};
+  static constexpr int kKind[6] = {KD_GEMM_FWD_LSE, KD_GEMM_BWD_DZ, KD_GEMM_DW, KD_GEMM_DW,
+                                   KD_GEMM_DH, KD_GEMM_FWD_LSE};
   auto kern = gemm2_kernel<Elem, A_MN, B_MN, EPI>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        GEMM2_SMEM_BYTES);
@@ -653,6 +727,26 @@ WsLayout ws_layout(int64_t T, int64_t d, int64_t V, int K, int64_t chunk, int dt
   return L;
 }
 
+KeepLayout keep_layout(int64_t T, int64_t d, int64_t V, int64_t chunk, int64_t fwd_chunk,
+                       int dtype) {
+  KeepLayout K;
+  const WsLayout L = ws_layout(T, d, V, 1, chunk, dtype);
+  CheckedSize c;
+  c.ok = L.ok;
+  const size_t rows = static_cast<size_t>(fwd_chunk < T ? fwd_chunk : T);
+  size_t off = L.total;
+  K.part = off;
+  off = c.align(c.add(off, c.mul(c.mul(rows, static_cast<size_t>((V + BN - 1) / BN)), 16)));
+  K.ld_max = (T + 31) / 32 * 32;
+  K.block_max = off;
+  off = c.align(c.add(off, c.mul(c.mul(static_cast<size_t>((V + 31) / 32),
+                                       static_cast<size_t>(K.ld_max)), 4)));
+  K.total = off;
+  K.ok = c.ok;
+  if (!K.ok) K.total = SIZE_MAX;
+  return K;
+}
+
 template <typename Elem>
 static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_norm, int64_t d,
                           int64_t V, const RowTerms& rt, int64_t chunk, float tau, float* loss,
@@ -667,7 +761,10 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   float* p_s = reinterpret_cast<float*>(w + L.p_sorted);
   float2* stats = reinterpret_cast<float2*>(w + L.stats);
   float* row = row_out ? row_out : reinterpret_cast<float*>(w + L.kl);
-  float4* part = reinterpret_cast<float4*>(w + L.scratch);
+  const bool keep = rt.keep_chunk > 0;
+  KeepLayout K;
+  if (keep) K = keep_layout(T, d, V, rt.keep_chunk, chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
+  float4* part = reinterpret_cast<float4*>(w + (keep ? K.part : L.scratch));
 
   if (cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return KD_ERR_CUDA;
   const float inv_tau = 1.f / tau;
@@ -701,12 +798,22 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
     g.partials = part;
     g.status = status;
     g.wait_limit_ns = limit_ns;
-    if (launch_gemm2<Elem, 0, 0, EPI_FWD_LSE>(tH, tW, tH /*no output box*/, g, s, num_sms) !=
-        cudaSuccess)
+    if (keep) {
+      CUtensorMap tE;
+      if (!make_out_map(&tE, reinterpret_cast<Elem*>(w + L.scratch) + c0 * L.ldz, F32, V, rows,
+                        L.ldz))
+        return KD_ERR_CUDA;
+      g.block_max = reinterpret_cast<float*>(w + K.block_max);
+      g.ld_max = K.ld_max;
+      if (launch_gemm2<Elem, 0, 0, EPI_FWD_KEEP>(tH, tW, tE, g, s, num_sms) != cudaSuccess)
+        return KD_ERR_CUDA;
+    } else if (launch_gemm2<Elem, 0, 0, EPI_FWD_LSE>(tH, tW, tH /*no output box*/, g, s,
+                                                     num_sms) != cudaSuccess) {
       return KD_ERR_CUDA;
+    }
     const int cblocks = cdiv(rows * 32, 256);
     if (launch_pdl(rt.targets ? combine_kernel<true> : combine_kernel<false>,
-                   static_cast<unsigned>(cblocks), 256u, s, static_cast<const float4*>(part),
+                   dim3(cblocks), 256u, s, static_cast<const float4*>(part),
                    static_cast<int>(rows), g.n_tiles, c0, zscale, inv_tau,
                    static_cast<const float2*>(stats), lse, row) != cudaSuccess)
       return KD_ERR_CUDA;
@@ -753,6 +860,18 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   // updated once per group with K = the group's rows (halving dW's
   // read-modify-write traffic); dz and dH are formed chunk by chunk.
   const int64_t group_rows = chunk * KD_DW_GROUP;
+  const bool kept = rt.kept_logp != nullptr;   // then one group holds all rows
+  if (kept) {
+    const KeepLayout K =
+        keep_layout(T, d, V, chunk, rt.keep_chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
+    const int cols = cdiv(V, 32 * (16 / sizeof(Elem)));
+    const dim3 grid(cdiv(T, KEPT_ROWS), cols < 65535 ? cols : 65535);
+    if (launch_pdl(kept_dz_kernel<Elem>, grid, 256u, s, dz, L.ldz, T, V, zscale, inv_T_tau,
+                   reinterpret_cast<const float*>(w + K.block_max), K.ld_max, lse, rt.kept_logp,
+                   grad_loss, static_cast<const int32_t*>(idx_s),
+                   static_cast<const float2*>(stats)) != cudaSuccess)
+      return KD_ERR_CUDA;
+  }
   for (int64_t g0 = 0; g0 < T; g0 += group_rows) {
     const int64_t grows = (T - g0) < group_rows ? (T - g0) : group_rows;
     for (int64_t off = 0; off < grows; off += chunk) {
@@ -765,7 +884,8 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
       if (!make_map(&tH_k, hc, F32, d, rows, d, BK, BM)) return KD_ERR_CUDA;
       if (!make_map(&tDz_k, dzc, F32, V, rows, L.ldz, BK, BM)) return KD_ERR_CUDA;
 
-      // (1) recompute z = h_c W^T; epilogue writes dz_c [rows, ldz]
+      // (1) recompute z = h_c W^T; epilogue writes dz_c [rows, ldz] (unless the
+      //     forward kept its exponentials, of which dz was made above)
       GemmArgs g;
       memset(&g, 0, sizeof(g));
       g.M = static_cast<int32_t>(rows);
@@ -790,7 +910,8 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
       g.ldo = L.ldz;
       g.status = status;
       g.wait_limit_ns = limit_ns;
-      if (launch_gemm2<Elem, 0, 0, EPI_BWD_DZ>(tH_k, tW_k, tDz_out, g, s, num_sms) != cudaSuccess)
+      if (!kept &&
+          launch_gemm2<Elem, 0, 0, EPI_BWD_DZ>(tH_k, tW_k, tDz_out, g, s, num_sms) != cudaSuccess)
         return KD_ERR_CUDA;
 
       if (!dH) continue;             // the caller wants dW alone
@@ -820,7 +941,7 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
         const int64_t n4 = rows * (d / 4);
         int64_t blocks = (n4 + 255) / 256;
         if (blocks > 4 * static_cast<int64_t>(num_sms)) blocks = 4 * static_cast<int64_t>(num_sms);
-        if (launch_pdl(dh_reduce_kernel<Elem>, static_cast<unsigned>(blocks), 256u, s,
+        if (launch_pdl(dh_reduce_kernel<Elem>, dim3(static_cast<unsigned>(blocks)), 256u, s,
                        static_cast<const float*>(hpart), gh.k_split,
                        static_cast<int64_t>(L.rows_pad), static_cast<int>(rows), d,
                        static_cast<Elem*>(dH) + c0 * d) != cudaSuccess)

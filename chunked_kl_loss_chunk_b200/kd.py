@@ -37,6 +37,7 @@ KD_ERR_BAD_INDEX, KD_ERR_TIMEOUT, KD_ERR_CUDA, KD_ERR_INTERNAL = 4, 5, 6, 7
 KD_DTYPE_F32, KD_DTYPE_BF16 = 0, 1
 KD_KL_LOGPROB_CACHE, KD_KL_TAU_SQUARED = 0x1, 0x2
 KD_TARGET_IGNORE = -100
+KD_HEAD_FWD, KD_HEAD_BOTH, KD_HEAD_KEEP = 0, 1, 2
 KD_REDUCE_TOKEN, KD_REDUCE_SEQUENCE, KD_REDUCE_FIXED = 0, 1, 2
 KD_PREF_SIGMOID, KD_PREF_HINGE, KD_PREF_IPO = 0, 1, 2
 REDUCTIONS = {"token": KD_REDUCE_TOKEN, "sequence": KD_REDUCE_SEQUENCE, "fixed": KD_REDUCE_FIXED}
@@ -71,9 +72,9 @@ _SIGNATURES = {
                                        _c_vp, _c_vp, _c_int, _c_vp, _c_sz, _c_vp]),
     "kd_head_logprob_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_int]),
     "kd_head_logprob_fwd": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
-                                     ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
+                                     ctypes.c_float, _c_int, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
     "kd_head_logprob_bwd": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
-                                     ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
+                                     ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
                                      _c_vp, _c_sz, _c_vp]),
     "kd_policy_loss_workspace_size": (_c_sz, [_c_i64, _c_i64]),
     "kd_policy_loss": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_i64, _c_i64, _c_f64,
@@ -211,21 +212,21 @@ def kd_fused_kl_fwd_noalloc(h, W, dtype, T, d, V, t_vals, t_idx, K, chunk, tempe
                                           loss, lse, kl_rows, stream)
 
 
-def kd_head_logprob_workspace_size(T, d, V, chunk, dtype, backward):
-    return load().kd_head_logprob_workspace_size(T, d, V, chunk, dtype, backward)
+def kd_head_logprob_workspace_size(T, d, V, chunk, dtype, use):
+    return load().kd_head_logprob_workspace_size(T, d, V, chunk, dtype, use)
 
 
-def kd_head_logprob_fwd(h, W, dtype, T, d, V, targets, chunk, temperature, logp, lse, ws, ws_bytes,
-                        stream):
-    return load().kd_head_logprob_fwd(h, W, dtype, T, d, V, targets, chunk, temperature, logp, lse,
-                                      ws, ws_bytes, stream)
+def kd_head_logprob_fwd(h, W, dtype, T, d, V, targets, chunk, temperature, keep, logp, lse, ws,
+                        ws_bytes, stream):
+    return load().kd_head_logprob_fwd(h, W, dtype, T, d, V, targets, chunk, temperature, keep, logp,
+                                      lse, ws, ws_bytes, stream)
 
 
-def kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse, grad_logp, grad_loss,
-                        dH, dW, dW_dtype, accumulate_dW, ws, ws_bytes, stream):
+def kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse, kept_logp, grad_logp,
+                        grad_loss, dH, dW, dW_dtype, accumulate_dW, ws, ws_bytes, stream):
     return load().kd_head_logprob_bwd(h, W, dtype, T, d, V, targets, chunk, temperature, lse,
-                                      grad_logp, grad_loss, dH, dW, dW_dtype, accumulate_dW, ws,
-                                      ws_bytes, stream)
+                                      kept_logp, grad_logp, grad_loss, dH, dW, dW_dtype,
+                                      accumulate_dW, ws, ws_bytes, stream)
 
 
 def kd_policy_loss_workspace_size(n_seqs, n_tokens):
@@ -547,38 +548,43 @@ def _head_sizes(h, W, targets):
 
 
 def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, stream=None,
-                  backward: bool = False):
+                  backward: bool = False, keep: bool = False):
     """Log-probabilities of one token per position through the output head, the
     [T, V] logits never materialised: (logp f32 [T], lse f32 [T], ws).
 
     ``targets`` int32 [T]; KD_TARGET_IGNORE (-100) marks positions without a
     token (logp 0, no gradient).  ``backward=True`` sizes the workspace for
-    ``head_logprobs_bwd`` as well, which takes ``lse`` and may take ``ws``."""
+    ``head_logprobs_bwd`` as well, which takes ``lse`` and may take ``ws``.
+    ``keep=True`` (T <= 2 chunk) leaves in ``ws`` what one backward needs of the
+    logits, which then does not project again: hand it ``ws`` and
+    ``kept_logp=logp``, and let nothing else use ``ws`` in between."""
     T, d, V, code = _head_sizes(h, W, targets)
     with _use_stream(h.device, stream):
         if ws is None:
-            ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, int(backward)),
-                                 h.device)
+            use = KD_HEAD_KEEP if keep else (KD_HEAD_BOTH if backward else KD_HEAD_FWD)
+            ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, use), h.device)
         else:
             _require("ws", ws, torch.uint8, (ws.numel(),), h.device)
         logp = torch.empty((T,), dtype=torch.float32, device=h.device)
         lse = torch.empty_like(logp)
         _check(kd_head_logprob_fwd(h.data_ptr(), W.data_ptr(), code, T, d, V, targets.data_ptr(),
-                                   chunk, float(temperature), logp.data_ptr(), lse.data_ptr(),
-                                   ws.data_ptr(), ws.numel(), _current_stream(h.device)),
+                                   chunk, float(temperature), bool(keep), logp.data_ptr(),
+                                   lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                                   _current_stream(h.device)),
                "kd_head_logprob_fwd")
     return logp, lse, ws
 
 
 def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: float = 1.0,
                       grad_loss=None, ws=None, dH=None, dW=None, accumulate_dW: bool = False,
-                      stream=None, need=(True, True), dW_dtype=torch.float32):
+                      stream=None, need=(True, True), dW_dtype=torch.float32, kept_logp=None):
     """Gradients of sum_t grad_logp[t] * logp[t] (times the device scalar
     ``grad_loss``): (dH [T, d] dtype of h, dW [V, d] f32, ws).  The logits are
     recomputed chunk by chunk; ``accumulate_dW=True`` adds into a given dW;
     ``dW_dtype=torch.bfloat16`` gives a bf16 dW where T <= 2 chunk.
     ``need=(dH, dW)`` leaves out a gradient that is not wanted (None in its
-    place)."""
+    place).  ``kept_logp`` and ``ws`` of a forward with ``keep=True``: its
+    exponentials take the place of recomputed logits, and are used up."""
     T, d, V, code = _head_sizes(h, W, targets)
     _require("lse", lse, torch.float32, (T,), h.device)
     _require("grad_logp", grad_logp, torch.float32, (T,), h.device)
@@ -586,6 +592,10 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
         _require("grad_loss", grad_loss, torch.float32, grad_loss.shape, h.device)
         if grad_loss.numel() != 1:
             raise ValueError("grad_loss: one value is needed")
+    if kept_logp is not None:
+        _require("kept_logp", kept_logp, torch.float32, (T,), h.device)
+        if ws is None:
+            raise ValueError("kept_logp: needs the workspace of its forward")
     if accumulate_dW and dW is None:
         raise ValueError("accumulate_dW: needs the dW to add to")
     if dW_dtype is not torch.float32 and dW_dtype is not torch.bfloat16:
@@ -594,7 +604,8 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
         raise ValueError("need: at least one gradient")
     with _use_stream(h.device, stream):
         if ws is None:
-            ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, 1), h.device)
+            ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, KD_HEAD_BOTH),
+                                 h.device)
         else:
             _require("ws", ws, torch.uint8, (ws.numel(),), h.device)
         if not need[0]:
@@ -610,7 +621,8 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
         else:
             _require("dW", dW, dW_dtype, (V, d), h.device)
         _check(kd_head_logprob_bwd(h.data_ptr(), W.data_ptr(), code, T, d, V, targets.data_ptr(),
-                                   chunk, float(temperature), lse.data_ptr(), grad_logp.data_ptr(),
+                                   chunk, float(temperature), lse.data_ptr(), _ptr(kept_logp),
+                                   grad_logp.data_ptr(),
                                    _ptr(grad_loss), _ptr(dH), _ptr(dW),
                                    KD_DTYPE_BF16 if dW_dtype is torch.bfloat16 else KD_DTYPE_F32,
                                    int(accumulate_dW), ws.data_ptr(), ws.numel(), _current_stream(h.device)),
@@ -621,24 +633,31 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
 class HeadLogprobs(torch.autograd.Function):
     """``logp = HeadLogprobs.apply(h, W, targets, chunk, temperature)``: the
     log-probabilities of ``head_logprobs`` with gradients to h and W (W's in
-    W's dtype)."""
+    W's dtype).  Up to two chunks of positions the forward keeps what the
+    backward needs of the logits (2 V bytes per position for bf16, in the
+    workspace that the backward needs anyway); beyond, the backward recomputes
+    them chunk by chunk."""
 
     @staticmethod
     def forward(ctx, h, W, targets, chunk, temperature=1.0):
-        logp, lse, _ = head_logprobs(h, W, targets, chunk, temperature)
-        ctx.save_for_backward(h, W, targets, lse)
+        keep = any(ctx.needs_input_grad[:2]) and h.shape[0] <= 2 * chunk
+        logp, lse, ws = head_logprobs(h, W, targets, chunk, temperature, keep=keep)
+        ctx.save_for_backward(h, W, targets, lse, logp if keep else None)
         ctx.chunk, ctx.temperature = chunk, temperature
+        ctx.ws = ws if keep else None
         return logp
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g):
-        h, W, targets, lse = ctx.saved_tensors
+        h, W, targets, lse, kept = ctx.saved_tensors
+        ws, ctx.ws = ctx.ws, None        # used up: a second backward recomputes
         # dW leaves the kernel in W's type where it is formed in one go, and is added up in fp32
         # and rounded afterwards otherwise
         direct = h.shape[0] <= 2 * ctx.chunk
         dH, dW, _ = head_logprobs_bwd(h, W, targets, lse, g.contiguous(), ctx.chunk, ctx.temperature,
-                                      need=ctx.needs_input_grad[:2],
+                                      need=ctx.needs_input_grad[:2], ws=ws,
+                                      kept_logp=None if ws is None else kept,
                                       dW_dtype=W.dtype if direct else torch.float32)
         return dH, None if dW is None else dW.to(W.dtype), None, None, None
 

@@ -31,12 +31,18 @@ class Step(NamedTuple):
 
 def _through_head(h, W, targets, objective, chunk, temperature, ws, dW, accumulate_dW):
     flat = targets.reshape(-1)
-    logp, lse, ws = kd.head_logprobs(h, W, flat, chunk, temperature, ws=ws, backward=True)
-    logp = logp.view(targets.shape)
-    loss, extra, dlogp = objective(logp, targets != kd.KD_TARGET_IGNORE)
+    # up to two chunks the forward keeps what the backward needs of the logits (a given workspace
+    # decides by its size)
+    keep = h.shape[0] <= 2 * chunk
+    if keep and ws is not None:
+        keep = ws.numel() >= kd.kd_head_logprob_workspace_size(*h.shape, W.shape[0], chunk, kd._dtype_code(h),
+                                                               kd.KD_HEAD_KEEP)
+    logp, lse, ws = kd.head_logprobs(h, W, flat, chunk, temperature, ws=ws, backward=True, keep=keep)
+    shaped = logp.view(targets.shape)
+    loss, extra, dlogp = objective(shaped, targets != kd.KD_TARGET_IGNORE)
     dH, dW, _ = kd.head_logprobs_bwd(h, W, flat, lse, dlogp.view(-1), chunk, temperature, ws=ws, dW=dW,
-                                     accumulate_dW=accumulate_dW)
-    return Step(loss, extra, logp, dH, dW, ws)
+                                     accumulate_dW=accumulate_dW, kept_logp=logp if keep else None)
+    return Step(loss, extra, shaped, dH, dW, ws)
 
 
 def policy_step(h, W, targets, old_logp, advantages, *, chunk: int, temperature: float = 1.0, ref_logp=None,

@@ -253,24 +253,36 @@ kd_status kd_fused_kl_bwd_shard(const void* h, const void* W, int dtype,
 /* A row with this target has no token: its logp is 0 and its gradient 0. */
 #define KD_TARGET_IGNORE (-100)
 
-/* Bytes of workspace: backward == 0 for kd_head_logprob_fwd alone (16 bytes per
- * row of max(chunk, 2048) and 256 vocabulary entries, and 20 per position),
- * otherwise for both calls. */
+/* Bytes of workspace, by what it is for:
+ *   KD_HEAD_FWD   kd_head_logprob_fwd alone: 16 bytes per row of max(chunk, 2048)
+ *                 and 256 vocabulary entries, and 20 per position;
+ *   KD_HEAD_BOTH  both calls: as kd_fused_kl_workspace_size (dz of two chunks);
+ *   KD_HEAD_KEEP  both calls, the forward keeping what the backward needs of the
+ *                 logits: about 5 V bytes per position of at most two chunks more
+ *                 than the dz it lies in.  T <= 2 chunk (0 otherwise). */
+#define KD_HEAD_FWD 0
+#define KD_HEAD_BOTH 1
+#define KD_HEAD_KEEP 2
 size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int dtype,
-                                      int backward);
+                                      int use);
 
 /*
  * Forward.  h, W, dtype, T, d, V, chunk, temperature as for kd_fused_kl_fwd;
  *   targets [T] int32: y_t in [0, V), or KD_TARGET_IGNORE
  * Outputs (device): logp float32 [T], lse float32 [T] (of every row; keep it
  * for the backward).  Bit-identical for every `chunk`, of which the forward
- * takes several in one launch where they are below 2048 rows.  A target outside [0, V)
+ * takes several in one launch where they are below 2048 rows.
+ * keep != 0 (T <= 2 chunk, else KD_ERR_UNSUPPORTED; KD_HEAD_KEEP's workspace)
+ * leaves the exponentials of the logits in ws, in the operands' type, for ONE
+ * kd_head_logprob_bwd on the same ws, inputs and sizes: it then need not project
+ * again.  Nothing else may use ws in between.  A target outside [0, V)
  * other than KD_TARGET_IGNORE is recorded as KD_ERR_BAD_INDEX; the outputs of
  * that call are then unspecified.
  */
 kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
-                              float* logp, float* lse, void* ws, size_t ws_bytes, void* stream);
+                              int keep, float* logp, float* lse, void* ws, size_t ws_bytes,
+                              void* stream);
 
 /*
  * Backward for the gradient grad_logp [T] float32 of each row's log-probability
@@ -281,14 +293,17 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
  *   or KD_DTYPE_BF16 for bf16 operands, rounded once from the fp32 sum, where
  *   one is formed: T <= 2 chunk and accumulate_dW == 0 (KD_ERR_UNSUPPORTED
  *   otherwise).
+ * kept_logp: the logp of the forward that kept its exponentials in this ws, which
+ * this call uses up; NULL: the logits are recomputed.  The kept ones are rounded
+ * once more (each dz entry but the target's has two roundings in place of one).
  * Either of dH and dW may be NULL: that gradient is not computed (a frozen head
  * needs no dW).  dz is rounded to the operands' type, as in kd_fused_kl_bwd.  An ignored row
  * contributes 0 times its h to dW, so h must be finite in every row.
  */
 kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
-                              const float* lse, const float* grad_logp, const float* grad_loss,
-                              void* dH, void* dW, int dW_dtype, int accumulate_dW, void* ws,
+                              const float* lse, const float* kept_logp, const float* grad_logp,
+                              const float* grad_loss, void* dH, void* dW, int dW_dtype, int accumulate_dW, void* ws,
                               size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */

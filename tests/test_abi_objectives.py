@@ -19,13 +19,13 @@ def lib():
 
 
 def _head(call, **kw):
-    a = dict(h=FAKE, W=FAKE, dtype=kd.KD_DTYPE_BF16, T=256, d=256, V=4096, targets=FAKE, chunk=64, tau=1.0,
+    a = dict(h=FAKE, W=FAKE, dtype=kd.KD_DTYPE_BF16, T=256, d=256, V=4096, targets=FAKE, chunk=64, tau=1.0, keep=0,
              logp=FAKE, lse=FAKE, g=FAKE, gl=None, dH=FAKE, dW=FAKE, dWt=0, acc=0, ws=FAKE, ws_bytes=1 << 40)
     a.update(kw)
     head = (a["h"], a["W"], a["dtype"], a["T"], a["d"], a["V"], a["targets"], a["chunk"], a["tau"])
     if call == "fwd":
-        return kd.kd_head_logprob_fwd(*head, a["logp"], a["lse"], a["ws"], a["ws_bytes"], None)
-    return kd.kd_head_logprob_bwd(*head, a["lse"], a["g"], a["gl"], a["dH"], a["dW"], a["dWt"], a["acc"], a["ws"],
+        return kd.kd_head_logprob_fwd(*head, a["keep"], a["logp"], a["lse"], a["ws"], a["ws_bytes"], None)
+    return kd.kd_head_logprob_bwd(*head, a["lse"], FAKE if a["keep"] else None, a["g"], a["gl"], a["dH"], a["dW"], a["dWt"], a["acc"], a["ws"],
                                   a["ws_bytes"], None)
 
 
@@ -38,6 +38,10 @@ def test_head_logprob_refusals(call):
     for kw in (dict(dtype=7), dict(d=12), dict(V=2 ** 31), dict(T=1 << 40), dict(T=1 << 31, chunk=1 << 31)):
         assert _head(call, **kw) == kd.KD_ERR_UNSUPPORTED, kw
     assert _head(call, ws_bytes=1024) == kd.KD_ERR_WORKSPACE
+    # what the forward keeps has to fit one group of two chunks, and its workspace
+    assert _head(call, keep=1, chunk=127) == kd.KD_ERR_UNSUPPORTED
+    assert _head(call, keep=1, chunk=128, ws_bytes=kd.kd_head_logprob_workspace_size(256, 256, 4096, 128, 1, 1)) \
+        == kd.KD_ERR_WORKSPACE
     if call == "fwd":
         assert _head(call, logp=None) == kd.KD_ERR_INVALID_ARG
     else:
@@ -56,6 +60,8 @@ def test_head_workspace_sizes():
     assert 0 < fwd < 20 << 20 and both >= 2 * 2048 * 131072 * 2
     assert both == kd.kd_fused_kl_workspace_size(2048, 4096, 131072, 1, 2048, kd.KD_DTYPE_BF16)
     assert size(0, 8, 8, 1, 1, 0) == 0
+    kept = size(2048, 4096, 131072, 2048, kd.KD_DTYPE_BF16, kd.KD_HEAD_KEEP)
+    assert both < kept <= both + 2048 * 131072 // 4 and size(300, 64, 500, 149, 1, kd.KD_HEAD_KEEP) == 0
     # the forward's need is refused by the backward, and accepted by the forward's own check
     assert _head("bwd", ws_bytes=kd.kd_head_logprob_workspace_size(256, 256, 4096, 64, 1, 0)) == kd.KD_ERR_WORKSPACE
 

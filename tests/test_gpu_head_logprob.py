@@ -83,6 +83,40 @@ def test_forward_and_gradients(T, d, V, chunk, dtype, tau):
     assert bool(((dH.double() - rH).abs() <= 2 * eps * aH + delta * pH + 1e-30).all())
     assert bool(((dW.double() - rW).abs() <= eps * aW + delta * pW + 1e-30).all())
     assert bool((dH[tgt < 0] == 0).all())
+    if T <= 2 * chunk:
+        # the forward keeps its exponentials: the same logp, one rounding more in dz
+        kl, klse, kws = kd.head_logprobs(h, W, tgt, chunk, tau, keep=True)
+        assert torch.equal(kl, logp) and torch.equal(klse, lse)
+        kH, kW, _ = kd.head_logprobs_bwd(h, W, tgt, klse, g, chunk, tau, ws=kws, kept_logp=kl)
+        assert kd.read_device_status(kws) == kd.KD_OK
+        assert bool(((kH.double() - rH).abs() <= 3 * eps * aH + delta * pH + 1e-30).all())
+        assert bool(((kW.double() - rW).abs() <= 2 * eps * aW + delta * pW + 1e-30).all())
+        assert bool((kH[tgt < 0] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_kept_exponentials_of_confident_rows(dtype):
+    """Rows that give their target nearly all the mass, or none, logits that are far
+    apart, and a head with a ragged last block: the target's entry keeps its digits."""
+    require_gpu()
+    T, d, V, chunk = 96, 64, 1003, 64
+    gen = torch.Generator("cuda").manual_seed(4)
+    W = torch.randn((V, d), generator=gen, device="cuda").to(dtype)
+    tgt = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    tgt[:4] = torch.tensor([0, V - 1, 31, 32], device="cuda")
+    h = W[tgt.long()].float()
+    h[1::2] *= 0.15
+    h[2::4] *= -1.0
+    h = h.to(dtype)
+    g = torch.randn((T,), generator=gen, device="cuda")
+    logp, lse, ws = kd.head_logprobs(h, W, tgt, chunk, keep=True)
+    assert logp.max().item() > -1e-3 and logp.min().item() < -50
+    dH, dW, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk, ws=ws, kept_logp=logp)
+    rl, rlse, rH, rW, aH, aW, pH, pW = _plain(h, W, tgt, 1.0, g)
+    # logits up to about 100: d 2^-24 sum|h w| of them, below 4e-4 (tf32: 2^-10 of sum|h w|, 0.2)
+    delta = 4e-4 if dtype is torch.bfloat16 else 0.3
+    assert bool(((dH.double() - rH).abs() <= 3 * 2 ** -8 * aH + 2 * delta * pH + 1e-30).all())
+    assert bool(((dW.double() - rW).abs() <= 2 * 2 ** -8 * aW + 2 * delta * pW + 1e-30).all())
 
 
 def test_every_row_ignored():
@@ -146,6 +180,7 @@ def test_autograd_frozen_head_and_accumulation():
     _, lse, _ = kd.head_logprobs(h, W, tgt, 48)
     dH, dW, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, 48)
     hl, Wl = h.clone().requires_grad_(), W.clone().requires_grad_()
+    # (130 positions in chunks of 48 are more than two chunks: recomputed)
     gh, gw = torch.autograd.grad(kd.HeadLogprobs.apply(hl, Wl, tgt, 48, 1.0), (hl, Wl), g)
     assert torch.equal(gh, dH) and torch.equal(gw, dW.to(torch.bfloat16))
     # formed in one go, dW leaves the kernel in bf16: the rounding of the fp32 one
@@ -153,7 +188,14 @@ def test_autograd_frozen_head_and_accumulation():
         _, w32, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk)
         _, w16, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk, dW_dtype=torch.bfloat16)
         assert w16.dtype is torch.bfloat16 and torch.equal(w16, w32.to(torch.bfloat16))
-        gh, gw = torch.autograd.grad(kd.HeadLogprobs.apply(hl, Wl, tgt, chunk, 1.0), (hl, Wl), g)
+        kept, klse, ws = kd.head_logprobs(h, W, tgt, chunk, keep=True)
+        kH, kW, _ = kd.head_logprobs_bwd(h, W, tgt, klse, g, chunk, ws=ws, kept_logp=kept, dW_dtype=torch.bfloat16)
+        out = kd.HeadLogprobs.apply(hl, Wl, tgt, chunk, 1.0)
+        gh, gw = torch.autograd.grad(out, (hl, Wl), g, retain_graph=True)
+        assert torch.equal(gh, kH) and torch.equal(gw, kW)
+        # what was kept is used up: a second backward recomputes
+        gh, gw = torch.autograd.grad(out, (hl, Wl), g)
+        assert torch.equal(gh, kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk)[0])
         assert torch.equal(gw, w16)
     with pytest.raises(kd.KDError):
         kd.head_logprobs_bwd(h, W, tgt, lse, g, 64, dW_dtype=torch.bfloat16)
@@ -220,5 +262,11 @@ def test_refusals():
         kd.head_logprobs_bwd(h, W, tgt, lse, g, 8, accumulate_dW=True)
     with pytest.raises(ValueError):
         kd.head_logprobs_bwd(h, W, tgt, lse, g, 8, need=(False, False))
+    with pytest.raises(ValueError):
+        kd.head_logprobs_bwd(h, W, tgt, lse, g, 8, kept_logp=lse)
+    with pytest.raises(kd.KDError):
+        kd.head_logprobs(h, W, tgt, 7, keep=True)                        # more than two chunks
+    with pytest.raises(kd.KDError):
+        kd.head_logprobs(h, W, tgt, 8, keep=True, ws=kd.head_logprobs(h, W, tgt, 8, backward=True)[2])
     with pytest.raises(TypeError):
         kd.head_logprobs_bwd(h, W, tgt, lse, g.double(), 8)

@@ -3,8 +3,9 @@ one after the other, as a training program calls them.
 
 Each stage is compared with its plain fp64 form on what the stage before it gave
 (a logp off by a rounding may otherwise move a token across a clipping border).
-Tolerances: those of the stages' own tests (dH: two roundings to bf16, 2^-7 of
-sum|dz w|, and the logits' error, 2e-3 of the part that scales with p; dW: one).
+Tolerances: those of the stages' own tests (dH: up to three roundings to bf16,
+2^-8 of sum|dz w| each, where the forward keeps its exponentials, and the logits'
+error, 2e-3 of the part that scales with p; dW: up to two).
 """
 
 import numpy as np
@@ -40,8 +41,8 @@ def _check_head(step, h, W, tgt, tau, dlogp):
     rl, _, rH, rW, aH, aW, pH, pW = _plain(h, W, tgt.reshape(-1), tau, dlogp.reshape(-1))
     delta = 2e-3 / tau
     assert (step.logp.reshape(-1).double() - rl).abs().max() <= delta
-    assert bool(((step.dH.double() - rH).abs() <= 2 ** -7 * aH + delta * pH + 1e-30).all())
-    assert bool(((step.dW.double() - rW).abs() <= 2 ** -8 * aW + delta * pW + 1e-30).all())
+    assert bool(((step.dH.double() - rH).abs() <= 3 * 2 ** -8 * aH + delta * pH + 1e-30).all())
+    assert bool(((step.dW.double() - rW).abs() <= 2 * 2 ** -8 * aW + delta * pW + 1e-30).all())
 
 
 @pytest.mark.parametrize("tau", [1.0, 0.8])
@@ -86,11 +87,11 @@ def test_micro_batches_add_up():
     require_gpu()
     h, W, tgt, _, old, _, adv = _batch("rows", 64, 700, 7)
     n = float((tgt != kd.KD_TARGET_IGNORE).sum())
-    whole = posttrain.policy_step(h, W, tgt, old, adv, chunk=64)
+    whole = posttrain.policy_step(h, W, tgt, old, adv, chunk=32)
     dW, loss = None, 0.0
     for k in (0, 3):
         rows = slice(37 * k, 37 * (k + 3))
-        part = posttrain.policy_step(h[rows], W, tgt[k:k + 3], old[k:k + 3], adv[k:k + 3], chunk=64,
+        part = posttrain.policy_step(h[rows], W, tgt[k:k + 3], old[k:k + 3], adv[k:k + 3], chunk=32,
                                      reduction="fixed", denom=n, dW=dW, accumulate_dW=dW is not None)
         dW, loss = part.dW, loss + part.loss.item()
         # the weights 1 / n differ by a rounding, which may move dz across one of bf16's
@@ -105,6 +106,7 @@ def test_micro_batches_add_up():
 def test_step_captured_in_a_graph():
     require_gpu()
     h, W, tgt, cu, old, ref, adv = _batch("packed", 64, 700, 9)
+    # of the size that keeps nothing: the step then recomputes
     ws = kd.alloc_workspace(kd.kd_head_logprob_workspace_size(tgt.numel(), 64, 700, 64, kd.KD_DTYPE_BF16, 1), h.device)
 
     def run():
