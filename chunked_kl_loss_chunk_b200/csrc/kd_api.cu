@@ -106,7 +106,7 @@ const char* kd_status_string(int status) {
   }
 }
 
-int kd_version(void) { return (1 << 16) | 0; }
+int kd_version(void) { return (1 << 16) | 1; }
 
 size_t kd_topk_workspace_size(int64_t T, int64_t V, int K) {
   (void)T;

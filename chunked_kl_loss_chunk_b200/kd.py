@@ -519,6 +519,15 @@ def _use_stream(device, stream):
     return torch.cuda.stream(stream)
 
 
+def _used_on(stream, tensors):
+    """Tells the allocator that a given stream reads or writes these tensors, so
+    that their memory is not handed out again before that stream is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _current_stream(device) -> int:
     # the raw handle: building a torch.cuda.Stream for it costs as much as the launch
     return torch._C._cuda_getCurrentRawStream(device.index)
@@ -572,6 +581,7 @@ def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, 
                                    lse.data_ptr(), ws.data_ptr(), ws.numel(),
                                    _current_stream(h.device)),
                "kd_head_logprob_fwd")
+    _used_on(stream, (h, W, targets, ws))
     return logp, lse, ws
 
 
@@ -627,6 +637,7 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
                                    KD_DTYPE_BF16 if dW_dtype is torch.bfloat16 else KD_DTYPE_F32,
                                    int(accumulate_dW), ws.data_ptr(), ws.numel(), _current_stream(h.device)),
                "kd_head_logprob_bwd")
+    _used_on(stream, (h, W, targets, lse, grad_logp, grad_loss, kept_logp, dH, dW, ws))
     return dH, dW, ws
 
 
@@ -727,6 +738,7 @@ def policy_loss(logp, old_logp, advantages, *, mask=None, ref_logp=None, cu_seql
                                   0.0 if denom is None else denom, loss.data_ptr(),
                                   stats.data_ptr(), _ptr(dlogp), at, nbytes, _current_stream(dev)),
                "kd_policy_loss")
+    _used_on(stream, (logp, old_logp, ref_logp, advantages, mask, cu_seqlens, ws))
     return loss, stats, dlogp
 
 
@@ -784,6 +796,7 @@ def preference_loss(logp, *, ref_logp=None, mask=None, cu_seqlens=None, kind: st
                                       loss.data_ptr(), rewards.data_ptr(), _ptr(dlogp), at, nbytes,
                                       _current_stream(dev)),
                "kd_preference_loss")
+    _used_on(stream, (logp, ref_logp, mask, cu_seqlens, ws))
     return loss, rewards, dlogp
 
 
@@ -843,6 +856,7 @@ def grad_sumsq(grads, stream=None):
         _check(lib.kd_grad_sumsq(ptrs.buffer_info()[0], sizes.buffer_info()[0], codes.buffer_info()[0], n,
                              out.data_ptr(), at, nbytes, _current_stream(dev)),
                "kd_grad_sumsq")
+    _used_on(stream, grads)
     return out
 
 
@@ -870,4 +884,5 @@ def clip_grad_norm(grads, max_norm: float, out=None, sumsq=None, stream=None):
                             codes.buffer_info()[0], n, max_norm, _ptr(sumsq), norm.data_ptr(), at,
                             nbytes, _current_stream(dev)),
                "kd_grad_clip")
+    _used_on(stream, grads + (out or []) + [sumsq])
     return norm

@@ -265,6 +265,19 @@ def test_bad_cu_seqlens_are_reported(name, bad):
     assert kd.read_device_status(ws) == kd.KD_OK
 
 
+def test_any_byte_but_0_counts():
+    require_gpu()
+    x = _make("rows-of-1000", 10, True)
+    gen = torch.Generator("cuda").manual_seed(1)
+    byte = torch.randint(1, 256, x["mask"].shape, generator=gen, device="cuda", dtype=torch.uint8)
+    byte = torch.where(x["mask"], byte, torch.zeros_like(byte))
+    for reduction in ("token", "sequence"):
+        a, b = (kd.policy_loss(x["logp"], x["old"], x["adv"], mask=m, reduction=reduction) for m in (x["mask"], byte))
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    a, b = (kd.preference_loss(x["logp"], mask=m, length_normalize=True) for m in (x["mask"], byte))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_autograd():
     require_gpu()
     x = _make("rows-of-129", 10, True)
