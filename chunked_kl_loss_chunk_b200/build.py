@@ -1,7 +1,8 @@
 """Build libkd.so (the C-ABI library) in-tree with nvcc for sm_100a.
 
 Usage: ``python -m chunked_kl_loss_chunk_b200.build`` (or ``build()``).
-The library is written next to this file so it travels with the repository.
+The library is written next to this file so it travels with the repository, and
+beside it _kd_native.so, the C++ half of the Python binding (torch's headers, g++).
 """
 
 from __future__ import annotations
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -20,6 +22,8 @@ LIB_PATH = os.path.join(PKG_DIR, "libkd.so")
 # Same sources with the device-side invariant checks on (-DKD_DEBUG=1): a failed
 # check records KD_ERR_INTERNAL in the workspace's status word.
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libkd_debug.so")
+NATIVE_SRC = os.path.join(CSRC, "kd_native.cpp")
+NATIVE_PATH = os.path.join(PKG_DIR, "_kd_native.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -53,10 +57,33 @@ def up_to_date(debug: bool = False) -> bool:
     return all(os.path.getmtime(p) <= t for p in deps())
 
 
+def build_native(force: bool = False, verbose: bool = False) -> str:
+    """Compile _kd_native.so against the installed torch; returns its path."""
+    newest = max(os.path.getmtime(p) for p in (NATIVE_SRC, os.path.join(INCLUDE, "kd.h")))
+    if not force and os.path.exists(NATIVE_PATH) and os.path.getmtime(NATIVE_PATH) >= newest:
+        return NATIVE_PATH
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = NATIVE_PATH + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in (INCLUDE, os.path.join(home, "include"), os.path.join(cuda, "include"),
+                                sysconfig.get_paths()["include"])),
+           NATIVE_SRC, "-o", tmp, "-L" + os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, NATIVE_PATH)
+    return NATIVE_PATH
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile every CUDA source into one shared library; returns its path.
     ``debug`` builds libkd_debug.so, with the device-side invariant checks."""
     lib = DEBUG_LIB_PATH if debug else LIB_PATH
+    build_native(force and not debug, verbose)
     if not force and up_to_date(debug):
         return lib
     nvcc = _nvcc()

@@ -42,6 +42,7 @@ KD_REDUCE_TOKEN, KD_REDUCE_SEQUENCE, KD_REDUCE_FIXED = 0, 1, 2
 KD_PREF_SIGMOID, KD_PREF_HINGE, KD_PREF_IPO = 0, 1, 2
 REDUCTIONS = {"token": KD_REDUCE_TOKEN, "sequence": KD_REDUCE_SEQUENCE, "fixed": KD_REDUCE_FIXED}
 PREFERENCE_KINDS = {"sigmoid": KD_PREF_SIGMOID, "hinge": KD_PREF_HINGE, "ipo": KD_PREF_IPO}
+ADVANTAGES_PER = ("sequence", "token")
 CACHE_KINDS = ("logits", "logprobs")
 
 _c_i64, _c_int, _c_sz, _c_vp, _c_u64 = ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_uint64
@@ -101,6 +102,12 @@ KD_GEMM_FWD_LSE, KD_GEMM_BWD_DZ, KD_GEMM_DH, KD_GEMM_DW = 1, 2, 4, 8
 GEMM_KIND_NAMES = {1: "fwd_lse", 2: "bwd_dz", 4: "dH", 8: "dW", 12: "dH+dW"}
 
 _lib = None
+_native = None
+# the entry points that _kd_native calls, in the order of its bind()
+_NATIVE_CALLS = ("kd_head_logprob_workspace_size", "kd_head_logprob_fwd",
+                 "kd_policy_loss_workspace_size", "kd_policy_loss",
+                 "kd_preference_loss_workspace_size", "kd_preference_loss",
+                 "kd_grad_clip_workspace_size", "kd_grad_clip")
 
 
 def header_symbols():
@@ -112,7 +119,7 @@ def header_symbols():
 
 def load():
     """Load libkd.so (raises if it is missing: there is no fallback)."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -122,7 +129,13 @@ def load():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    _lib = lib
+    try:
+        from chunked_kl_loss_chunk_b200 import _kd_native
+    except ImportError as e:
+        raise RuntimeError(f"_kd_native.so not built or not loadable ({e}); "
+                           "run chunked_kl_loss_chunk_b200.build") from e
+    _kd_native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS))
+    _lib, _native = lib, _kd_native
     return lib
 
 
@@ -544,6 +557,13 @@ def _workspace(ws, nbytes: int, like):
     return buf, (buf.data_ptr() + 1023) & ~1023, n
 
 
+def _native_result(out, where: str):
+    """Outputs of a call made by _kd_native, or the error that it returned."""
+    if out.__class__ is int:
+        raise KDError(out, where)
+    return out
+
+
 def _head_sizes(h, W, targets):
     if not (isinstance(h, torch.Tensor) and isinstance(W, torch.Tensor)) or h.dim() != 2 or W.dim() != 2:
         raise ValueError("h [T, d] and W [V, d] are needed")
@@ -567,10 +587,15 @@ def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, 
     ``keep=True`` (T <= 2 chunk) leaves in ``ws`` what one backward needs of the
     logits, which then does not project again: hand it ``ws`` and
     ``kept_logp=logp``, and let nothing else use ``ws`` in between."""
+    use = KD_HEAD_KEEP if keep else (KD_HEAD_BOTH if backward else KD_HEAD_FWD)
+    load()
+    if stream is None:
+        out = _native.head_logprobs(h, W, targets, chunk, temperature, use, ws)
+        if out is not None:
+            return _native_result(out, "kd_head_logprob_fwd")
     T, d, V, code = _head_sizes(h, W, targets)
     with _use_stream(h.device, stream):
         if ws is None:
-            use = KD_HEAD_KEEP if keep else (KD_HEAD_BOTH if backward else KD_HEAD_FWD)
             ws = alloc_workspace(kd_head_logprob_workspace_size(T, d, V, chunk, code, use), h.device)
         else:
             _require("ws", ws, torch.uint8, (ws.numel(),), h.device)
@@ -642,15 +667,21 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
 
 
 class HeadLogprobs(torch.autograd.Function):
-    """``logp = HeadLogprobs.apply(h, W, targets, chunk, temperature)``: the
+    """``logp = HeadLogprobs.apply(h, W, targets, chunk, temperature=1.0)``: the
     log-probabilities of ``head_logprobs`` with gradients to h and W (W's in
     W's dtype).  Up to two chunks of positions the forward keeps what the
     backward needs of the logits (2 V bytes per position for bf16, in the
     workspace that the backward needs anyway); beyond, the backward recomputes
     them chunk by chunk."""
 
+    @classmethod
+    def apply(cls, h, W, targets, chunk, temperature=1.0):
+        if not torch.is_grad_enabled():          # nothing will ask for what a forward keeps
+            return head_logprobs(h.detach(), W.detach(), targets, chunk, temperature)[0]
+        return super().apply(h, W, targets, chunk, temperature)
+
     @staticmethod
-    def forward(ctx, h, W, targets, chunk, temperature=1.0):
+    def forward(ctx, h, W, targets, chunk, temperature):
         keep = any(ctx.needs_input_grad[:2]) and h.shape[0] <= 2 * chunk
         logp, lse, ws = head_logprobs(h, W, targets, chunk, temperature, keep=keep)
         ctx.save_for_backward(h, W, targets, lse, logp if keep else None)
@@ -712,21 +743,28 @@ def policy_loss(logp, old_logp, advantages, *, mask=None, ref_logp=None, cu_seql
     ``reduction``: "token", "sequence" or "fixed" (with ``denom``).  ``stats``:
     tokens that count, and over them the means of the ratio, of "clipped" and
     of the KL estimate.  ``dlogp`` is what ``head_logprobs_bwd`` takes."""
+    lib = load()
+    if stream is None and reduction in REDUCTIONS and advantages_per in ADVANTAGES_PER and \
+            (reduction == "fixed") == (denom is not None):
+        out = _native.policy_loss(logp, old_logp, ref_logp, advantages, advantages_per == "token", mask,
+                                  cu_seqlens, clip_low, clip_high, kl_coef, REDUCTIONS[reduction],
+                                  0.0 if denom is None else denom, grad, ws)
+        if out is not None:
+            return _native_result(out, "kd_policy_loss")
     n_seqs, n = _sequences(logp, cu_seqlens, mask)
     dev = logp.device
     if reduction not in REDUCTIONS:
         raise ValueError(f"reduction must be one of {tuple(REDUCTIONS)}")
     if (reduction == "fixed") != (denom is not None):
         raise ValueError("denom: belongs to reduction=\"fixed\" and to no other")
-    if advantages_per not in ("sequence", "token"):
-        raise ValueError("advantages_per must be \"sequence\" or \"token\"")
+    if advantages_per not in ADVANTAGES_PER:
+        raise ValueError(f"advantages_per must be one of {ADVANTAGES_PER}")
     per_token = advantages_per == "token"
     _require("advantages", advantages, torch.float32, logp.shape if per_token else (n_seqs,), dev)
     if old_logp is not None:
         _require("old_logp", old_logp, torch.float32, logp.shape, dev)
     if ref_logp is not None:
         _require("ref_logp", ref_logp, torch.float32, logp.shape, dev)
-    lib = load()
     with _use_stream(dev, stream):
         keep, at, nbytes = _workspace(ws, lib.kd_policy_loss_workspace_size(n_seqs, n), logp)
         loss = logp.new_empty(())
@@ -774,6 +812,12 @@ def preference_loss(logp, *, ref_logp=None, mask=None, cu_seqlens=None, kind: st
     one.  ``ref_logp`` (None: no reference) and ``mask`` like ``logp``.  ``kind``:
     "sigmoid" (with ``label_smoothing``), "hinge" or "ipo".  ``pairs_total``: the
     pairs of the whole batch when these are a part of it."""
+    lib = load()
+    if stream is None and kind in PREFERENCE_KINDS:
+        out = _native.preference_loss(logp, ref_logp, mask, cu_seqlens, PREFERENCE_KINDS[kind], beta, margin,
+                                      label_smoothing, length_normalize, pairs_total, grad, ws)
+        if out is not None:
+            return _native_result(out, "kd_preference_loss")
     n_seqs, n = _sequences(logp, cu_seqlens, mask)
     dev = logp.device
     if n_seqs % 2:
@@ -783,7 +827,6 @@ def preference_loss(logp, *, ref_logp=None, mask=None, cu_seqlens=None, kind: st
     if ref_logp is not None:
         _require("ref_logp", ref_logp, torch.float32, logp.shape, dev)
     pairs = n_seqs // 2
-    lib = load()
     with _use_stream(dev, stream):
         keep, at, nbytes = _workspace(ws, lib.kd_preference_loss_workspace_size(pairs, n), logp)
         loss = logp.new_empty(())
@@ -866,17 +909,20 @@ def clip_grad_norm(grads, max_norm: float, out=None, sumsq=None, stream=None):
     it, f32 [].  ``grads``: float32 and bfloat16 CUDA tensors of any shapes, each
     contiguous.  ``sumsq`` fp64 []: the sum of squares to use, where the list is
     a part of what the norm is taken over (``dp.clip_grad_norm``)."""
-    grads = list(grads)
+    lib = load()
+    grads, out = list(grads), None if out is None else list(out)
+    if stream is None:
+        done = _native.clip_grad_norm(grads, out, max_norm, sumsq)
+        if done is not None:
+            return _native_result(done, "kd_grad_clip")[0]
     n, dev, ptrs, sizes, codes = _grad_arrays("grads", grads)
     outs = ptrs
     if out is not None:
-        out = list(out)
         m, out_dev, outs, out_sizes, out_codes = _grad_arrays("out", out)
         if m != n or out_dev != dev or out_sizes != sizes or out_codes != codes:
             raise ValueError("out: the sizes, types and device of grads are needed")
     if sumsq is not None:
         _require("sumsq", sumsq, torch.float64, (), dev)
-    lib = load()
     with _use_stream(dev, stream):
         keep, at, nbytes = _workspace(None, lib.kd_grad_clip_workspace_size(n), grads[0])
         norm = torch.empty((), dtype=torch.float32, device=dev)

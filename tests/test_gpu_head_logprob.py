@@ -199,6 +199,9 @@ def test_autograd_frozen_head_and_accumulation():
         assert torch.equal(gw, w16)
     with pytest.raises(kd.KDError):
         kd.head_logprobs_bwd(h, W, tgt, lse, g, 64, dW_dtype=torch.bfloat16)
+    with torch.no_grad():
+        plain = kd.HeadLogprobs.apply(hl, Wl, tgt, 130)
+    assert not plain.requires_grad and torch.equal(plain, kd.head_logprobs(h, W, tgt, 130)[0])
     hf = h.clone().requires_grad_()
     (only,) = torch.autograd.grad(kd.HeadLogprobs.apply(hf, W, tgt, 48, 1.0), (hf,), g)
     assert torch.equal(only, dH)
