@@ -258,12 +258,18 @@ prep_reg_kernel(const float* __restrict__ vals, const int32_t* __restrict__ idx,
 //   coef (S softmax - p [v == y])  is  g_t / tau ([v == y] - softmax),
 // the gradient of g_t logp_t.  A row whose target is KD_TARGET_IGNORE gets
 // p = S = 0 and an index past V (its g_t is not read); any other target outside
-// [0, V) gets the same and records KD_ERR_BAD_INDEX.
-__global__ void __launch_bounds__(256)
+// [0, V) gets the same and records KD_ERR_BAD_INDEX.  A single block also clears the
+// status word, in the place of a memset before it (2 us of a short call).
+constexpr int64_t PREP_ONE_BLOCK = 4096;      // rows
+__global__ void __launch_bounds__(1024)
 prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict__ grad, int64_t T,
                    int64_t V, int32_t* __restrict__ idx_sorted, float* __restrict__ p_sorted,
                    float2* __restrict__ stats, uint32_t* status) {
   griddep_launch_dependents();
+  if (gridDim.x == 1) {
+    if (threadIdx.x == 0) *status = 0u;
+    __syncthreads();
+  }
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < T;
        t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int32_t y = targets[t];
@@ -550,8 +556,8 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, unsigned block, cudaSt
   return cudaGetLastError();
 }
 
-// Row preparation for fwd_impl / bwd_impl.  One target per row: the target
-// kernel.  A cache with K <= 128: the register sort, a grid small enough to be
+// Row preparation for fwd_impl / bwd_impl, and the status word cleared before it.
+// One target per row: the target kernel.  A cache with K <= 128: the register sort, a grid small enough to be
 // resident at once, so that the first GEMM (launched with programmatic
 // serialization) can start while it runs.  Larger K: the shared-memory sort.
 cudaError_t launch_prep(const RowTerms& rt, int64_t T, int64_t V, float inv_tau, int32_t* idx_s,
@@ -559,10 +565,16 @@ cudaError_t launch_prep(const RowTerms& rt, int64_t T, int64_t V, float inv_tau,
   const int64_t blocks64 = (T + PREP_WARPS - 1) / PREP_WARPS;
   const int64_t cap = static_cast<int64_t>(num_sms) * 8;
   const int logprob = (rt.flags & KD_KL_LOGPROB_CACHE) ? 1 : 0;
+  const bool clears = rt.targets && T <= PREP_ONE_BLOCK;
+  if (!clears) {
+    const cudaError_t e = cudaMemsetAsync(status, 0, 4, s);
+    if (e != cudaSuccess) return e;
+  }
   if (rt.targets) {
-    const int64_t b = (T + 255) / 256;
-    prep_target_kernel<<<static_cast<unsigned>(b < cap ? b : cap), 256, 0, s>>>(
-        rt.targets, rt.grad_rows, T, V, idx_s, p_s, stats, status);
+    const int64_t b = clears ? 1 : (T + 1023) / 1024;
+    const int64_t threads = T < 1024 ? (T + 31) / 32 * 32 : 1024;
+    prep_target_kernel<<<static_cast<unsigned>(b < cap ? b : cap), static_cast<unsigned>(threads),
+                         0, s>>>(rt.targets, rt.grad_rows, T, V, idx_s, p_s, stats, status);
   } else if (rt.K <= PREP_REG_MAXK) {
     const unsigned blocks = static_cast<unsigned>(blocks64 < cap ? blocks64 : cap);
     prep_reg_kernel<<<blocks, PREP_WARPS * 32, 0, s>>>(rt.t_vals, rt.t_idx, T, rt.K, V, inv_tau,
@@ -766,7 +778,6 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   if (keep) K = keep_layout(T, d, V, rt.keep_chunk, chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
   float4* part = reinterpret_cast<float4*>(w + (keep ? K.part : L.scratch));
 
-  if (cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return KD_ERR_CUDA;
   const float inv_tau = 1.f / tau;
   if (launch_prep(rt, T, V, inv_tau, idx_s, p_s, stats, status, s, num_sms) != cudaSuccess)
     return KD_ERR_CUDA;
@@ -842,7 +853,6 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   float2* stats = reinterpret_cast<float2*>(w + L.stats);
   Elem* dz = reinterpret_cast<Elem*>(w + L.scratch);
 
-  if (cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return KD_ERR_CUDA;
   const float inv_tau = 1.f / tau;
   if (launch_prep(rt, T, V, inv_tau, idx_s, p_s, stats, status, s, num_sms) != cudaSuccess)
     return KD_ERR_CUDA;

@@ -236,7 +236,7 @@ __device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t* sm_flag) 
 // the main one.
 // ----------------------------------------------------------------------------
 constexpr int OBJ_THREADS = 256;
-constexpr int POLICY_STATS = 5;   // sums: loss, tokens, r, clipped, KL
+constexpr int POLICY_STATS = OBJ_PARTIALS;   // sums: loss, tokens, r, clipped, KL
 constexpr int PREF_BLOCKS_PER_SM = 4;
 constexpr int PREF_SHORT_MEAN = 30;   // tokens a sequence, on average, below which it is short
 constexpr int POLICY_BLOCKS_PER_SM = 3;
@@ -358,6 +358,7 @@ __device__ __forceinline__ void policy_count_each(const PolicyArgs& a, int32_t w
   const SeqLayout& q = a.seq;
   int32_t held_b = -1;
   uint32_t held = 0;
+  bool waited = false;               // for the kernel that clears the counts
   for (int64_t row = static_cast<int64_t>(warp) * 512; row < q.N;
        row += static_cast<int64_t>(n_warps) * 512) {
     const int32_t r0 = static_cast<int32_t>(row), t0 = r0 + lane * 16;   // below N + 512 < 2^31
@@ -365,6 +366,10 @@ __device__ __forceinline__ void policy_count_each(const PolicyArgs& a, int32_t w
     const Cursor first = cursor_at_warp(q, r0, lane);
     if (first.e >= min(r0 + 512, q.N)) {       // one sequence holds the 512
       if (first.b != held_b) {
+        if (held_b >= 0 && !waited) {
+          griddep_wait();
+          waited = true;
+        }
         policy_count_flush(a, held_b, held, lane);
         held_b = first.b;
         held = 0;
@@ -372,6 +377,8 @@ __device__ __forceinline__ void policy_count_each(const PolicyArgs& a, int32_t w
       held += __popc(m);
       continue;
     }
+    if (!waited) griddep_wait();
+    waited = true;
     Cursor c = first;
     if (t0 >= c.e && t0 < q.N) c = cursor_at(q, t0);
     int32_t pos = t0;
@@ -384,6 +391,7 @@ __device__ __forceinline__ void policy_count_each(const PolicyArgs& a, int32_t w
       if (pos < end) c = cursor_after(q, c, pos);
     }
   }
+  if (!waited) griddep_wait();
   policy_count_flush(a, held_b, held, lane);
 }
 
@@ -432,7 +440,11 @@ __device__ __forceinline__ void policy_fetch(const PolicyArgs& a, const PolicyQu
 // The masks of a warp's next rows, and the copies of those but the last under way.
 struct PolicyAhead {
   uint32_t m[POLICY_DEPTH + 1];
+  Cursor c;                         // of the next row, where sequences matter
 };
+__device__ __forceinline__ bool policy_by_sequence(const PolicyArgs& a) {
+  return a.reduction == KD_REDUCE_SEQUENCE || !a.adv_per_token;
+}
 template <bool OLD, bool REF>
 __device__ __forceinline__ void policy_start(const PolicyArgs& a, const PolicyQueue& rows,
                                              int32_t row, int32_t n_warps, PolicyAhead& ahead,
@@ -445,6 +457,8 @@ __device__ __forceinline__ void policy_start(const PolicyArgs& a, const PolicyQu
 #pragma unroll
   for (int k = 0; k < POLICY_DEPTH; ++k)
     policy_fetch<OLD, REF>(a, rows, k, row + k * n_warps, ahead.m[k], lane);
+  ahead.c = Cursor{0, INT_MAX};
+  if (policy_by_sequence(a) && row < n_rows) ahead.c = cursor_at_warp(a.seq, row * 128, lane);
 }
 
 __device__ __forceinline__ void policy_add(double (&v)[POLICY_STATS], const F2& loss,
@@ -460,8 +474,8 @@ __device__ __forceinline__ void policy_add(double (&v)[POLICY_STATS], const F2& 
 
 // The main pass.  A warp takes rows of 128 tokens, `row` and every n_warps-th
 // after it, the first of them under way (policy_start).  Sums go to v:
-// fp32 over at most 16 rows of a lane's tokens, then fp64 (a conversion to fp64
-// takes the time of 16 fp32 operations).  n_all: the tokens that count, for
+// fp32 over at most 16 rows of a lane's tokens, then fp64 (conversions to fp64 are
+// slow: see the gradients' sums).  n_all: the tokens that count, for
 // KD_REDUCE_TOKEN.
 template <bool OLD, bool REF>
 __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQueue& queue,
@@ -469,8 +483,7 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
                                               PolicyAhead& ahead, int lane,
                                               double (&v)[POLICY_STATS]) {
   const SeqLayout& q = a.seq;
-  const bool per_seq = a.reduction == KD_REDUCE_SEQUENCE;
-  const bool need_seq = per_seq || !a.adv_per_token;
+  const bool need_seq = policy_by_sequence(a);
   const int32_t first = seq_begin(q, 0), last = seq_begin(q, q.S), n_rows = rows_of(q);
   float w = a.inv_denom;
   if (a.reduction == KD_REDUCE_TOKEN) {
@@ -500,7 +513,7 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
 #pragma unroll
       for (int j = 0; j < 4; ++j) wt[j] = w;
       if (need_seq) {
-        const Cursor c = cursor_at_warp(q, row * 128, lane);
+        const Cursor c = ahead.c;
         if (c.e >= row * 128 + 128) {          // one sequence holds the row
           policy_look(a, c.b, seqs, at[0], wt[0]);
 #pragma unroll
@@ -578,6 +591,8 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
     if (a.dlogp && t0 < q.N) store4(a.dlogp, t0, q.N, out, a.vec);
     policy_fetch<OLD, REF>(a, queue, slot, row + POLICY_DEPTH * n_warps, ahead.m[POLICY_DEPTH - 1],
                            lane);
+    if (need_seq && row + n_warps < n_rows && __any_sync(0xffffffffu, ahead.m[0] != 0))
+      ahead.c = cursor_at_warp(q, (row + n_warps) * 128, lane);
   }
   policy_add(v, s_loss, s_ratio, s_kl);
   v[1] = n_tok;
@@ -607,6 +622,16 @@ __global__ void __launch_bounds__(OBJ_THREADS) policy_count_all_kernel(const Pol
     a.count[blockIdx.x] = n;
     if (blockIdx.x == 0) *a.status = *a.ticket = 0u;
   }
+}
+
+// Status, ticket and, for KD_REDUCE_SEQUENCE with a mask, the sequences' counts: a
+// kernel and not a memset, so that the next one can start under it.
+__global__ void __launch_bounds__(OBJ_THREADS) policy_clear_kernel(const PolicyArgs a,
+                                                                   int32_t counts) {
+  griddep_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * OBJ_THREADS + threadIdx.x;
+  if (i == 0) *a.status = *a.ticket = 0u;
+  if (i < counts) a.count[i] = 0u;
 }
 
 __global__ void __launch_bounds__(OBJ_THREADS) policy_count_each_kernel(const PolicyArgs a) {
@@ -1032,10 +1057,11 @@ __global__ void __launch_bounds__(OBJ_THREADS, 1) pref_one_kernel(const PrefArgs
 // ----------------------------------------------------------------------------
 namespace {
 
-// Batches of at most this many tokens and sequences run in one block.  (512, 4096 and
-// 8192 tokens: policy 5.4, 7.5 and 10.9 us in one block, 10.2 in several; preference
-// 5.2, 8.1 and 12.4 against 7.2, 8.4 and 8.5.)
-constexpr int64_t ONE_BLOCK_TOKENS = 4096, ONE_BLOCK_SEQUENCES = 1024;
+// Batches of at most this many tokens and sequences run in one block.  (8, 2048 and 4096
+// tokens: policy 4.3, 4.8 to 5.2 and 7 to 7.5 us in one block, 6.6 to 6.8 in several;
+// 8, 512, 1024 and 2048 tokens: preference 5.2, 5.3 to 6.2, 6.3 and 7.2 to 10 against 6.3,
+// 6.4 to 7.5, 8.1 and 6.7 to 7.8.)
+constexpr int64_t POLICY_ONE_BLOCK = 2048, PREF_ONE_BLOCK = 1024;
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), int64_t blocks, int threads, cudaStream_t s, bool pdl,
@@ -1064,7 +1090,7 @@ namespace {
 template <bool OLD, bool REF>
 kd_status policy_launch(PolicyArgs a, cudaStream_t s, int num_sms) {
   const SeqLayout& q = a.seq;
-  if (q.N <= ONE_BLOCK_TOKENS && q.S <= ONE_BLOCK_SEQUENCES)
+  if (q.N <= POLICY_ONE_BLOCK && q.S <= POLICY_ONE_BLOCK)
     return launch(policy_one_kernel<OLD, REF>, 1, OBJ_THREADS, s, false, a) == cudaSuccess
                ? KD_OK
                : KD_ERR_CUDA;
@@ -1077,19 +1103,19 @@ kd_status policy_launch(PolicyArgs a, cudaStream_t s, int num_sms) {
                 at_most(4 * num_sms, OBJ_MAX_COUNTS)));
     e = launch(policy_count_all_kernel, a.n_counts, OBJ_THREADS, s, false, a);
   } else {
-    // status, ticket and, right behind them, the sequences' counts
-    e = cudaMemsetAsync(a.status, 0,
-                        OBJ_HEADER + (each ? sizeof(uint32_t) * static_cast<size_t>(q.S) : 0), s);
+    const int32_t counts = each ? q.S : 0;
+    e = launch(policy_clear_kernel, (static_cast<int64_t>(counts) + OBJ_THREADS) / OBJ_THREADS,
+               OBJ_THREADS, s, false, a, counts);
     if (e == cudaSuccess && each)
       e = launch(policy_count_each_kernel,
                  at_most((static_cast<int64_t>(q.N) + 4095) / 4096, 4 * num_sms), OBJ_THREADS, s,
-                 false, a);
+                 true, a);
   }
   if (e != cudaSuccess) return KD_ERR_CUDA;
   const int64_t per_block = 4 * OBJ_THREADS;
   const int64_t cap = at_most(POLICY_BLOCKS_PER_SM * num_sms, OBJ_MAX_BLOCKS);
   e = launch(policy_main_kernel<OLD, REF>, at_most((q.N + per_block - 1) / per_block, cap),
-             OBJ_THREADS, s, all || each, a);
+             OBJ_THREADS, s, true, a);
   return e == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }
 
@@ -1107,7 +1133,7 @@ kd_status preference_loss(PrefArgs a, cudaStream_t s, int num_sms) {
   const SeqLayout& q = a.seq;
   constexpr int W = OBJ_THREADS / 32;
   // a warp for each pair as long as they last, then a lane
-  const bool one = q.N <= ONE_BLOCK_TOKENS && q.S <= ONE_BLOCK_SEQUENCES;
+  const bool one = q.N <= PREF_ONE_BLOCK && q.S <= PREF_ONE_BLOCK;
   const int64_t pairs = q.S / 2, warps = one ? W : static_cast<int64_t>(W) * 4 * num_sms;
   a.pairs_per_warp = static_cast<int32_t>(at_most((pairs + warps - 1) / warps, 32));
   // (2048 sequences of 8 tokens: 9 us with a lane each, 12 without; of 30: 10.4 and 10.3)

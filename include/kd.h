@@ -258,8 +258,8 @@ kd_status kd_fused_kl_bwd_shard(const void* h, const void* W, int dtype,
  *                 and 256 vocabulary entries, and 20 per position;
  *   KD_HEAD_BOTH  both calls: as kd_fused_kl_workspace_size (dz of two chunks);
  *   KD_HEAD_KEEP  both calls, the forward keeping what the backward needs of the
- *                 logits: about 5 V bytes per position of at most two chunks more
- *                 than the dz it lies in.  T <= 2 chunk (0 otherwise). */
+ *                 logits in the place of dz: about V / 5 bytes per position more
+ *                 than KD_HEAD_BOTH.  T <= 2 chunk (0 otherwise). */
 #define KD_HEAD_FWD 0
 #define KD_HEAD_BOTH 1
 #define KD_HEAD_KEEP 2
