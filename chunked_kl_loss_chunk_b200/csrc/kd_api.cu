@@ -272,9 +272,13 @@ static int64_t head_fwd_chunk(int64_t chunk) {
   return chunk > kd::KD_HEAD_FWD_ROWS ? chunk : kd::KD_HEAD_FWD_ROWS;
 }
 
+static int64_t head_bwd_chunk(int64_t chunk) {
+  return chunk > kd::KD_HEAD_BWD_ROWS ? chunk : kd::KD_HEAD_BWD_ROWS;
+}
+
 // Whether the backward forms dz of all T rows at once.
 static bool one_group(int64_t T, int64_t chunk) {
-  return (T + kd::KD_DW_GROUP - 1) / kd::KD_DW_GROUP <= chunk;
+  return (T + kd::KD_DW_GROUP - 1) / kd::KD_DW_GROUP <= head_bwd_chunk(chunk);
 }
 
 size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int dtype,
@@ -282,13 +286,13 @@ size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t c
   if (T < 1 || d < 1 || V < 1 || chunk < 1) return 0;
   if (use == KD_HEAD_KEEP) {
     if (!one_group(T, chunk)) return 0;
-    const kd::KeepLayout K = kd::keep_layout(T, d, V, chunk, head_fwd_chunk(chunk), dtype);
+    const kd::KeepLayout K = kd::keep_layout(T, d, V, head_bwd_chunk(chunk), head_fwd_chunk(chunk), dtype);
     return K.ok ? K.total : 0;
   }
   const kd::WsLayout F = kd::ws_layout(T, d, V, 1, head_fwd_chunk(chunk), dtype);
   if (!F.ok) return 0;
   if (use == KD_HEAD_FWD) return F.fwd_end;
-  const kd::WsLayout L = kd::ws_layout(T, d, V, 1, chunk, dtype);
+  const kd::WsLayout L = kd::ws_layout(T, d, V, 1, head_bwd_chunk(chunk), dtype);
   if (!L.ok) return 0;
   return L.total > F.fwd_end ? L.total : F.fwd_end;
 }
@@ -306,11 +310,11 @@ static kd_status validate_head(const void* h, const void* W, int dtype, int64_t 
   if (!ws || !aligned(ws, kd::KD_WS_ALIGN)) return KD_ERR_INVALID_ARG;
   if (keep) {
     if (!one_group(T, chunk)) return KD_ERR_UNSUPPORTED;
-    const kd::KeepLayout K = kd::keep_layout(T, d, V, chunk, head_fwd_chunk(chunk), dtype);
+    const kd::KeepLayout K = kd::keep_layout(T, d, V, head_bwd_chunk(chunk), head_fwd_chunk(chunk), dtype);
     return K.ok && ws_bytes >= K.total ? KD_OK : KD_ERR_WORKSPACE;
   }
   const kd::WsLayout L =
-      kd::ws_layout(T, d, V, 1, backward ? chunk : head_fwd_chunk(chunk), dtype);
+      kd::ws_layout(T, d, V, 1, backward ? head_bwd_chunk(chunk) : head_fwd_chunk(chunk), dtype);
   if (!L.ok || ws_bytes < (backward ? L.total : L.fwd_end)) return KD_ERR_WORKSPACE;
   return KD_OK;
 }
@@ -327,7 +331,7 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
   if (sms <= 0) return KD_ERR_CUDA;
   kd::RowTerms rt;
   rt.targets = targets;
-  rt.keep_chunk = keep ? chunk : 0;
+  rt.keep_chunk = keep ? head_bwd_chunk(chunk) : 0;
   return kd::fused_fwd(h, W, dtype, T, 1, d, V, rt, head_fwd_chunk(chunk), temperature, nullptr,
                        lse, logp, ws, static_cast<cudaStream_t>(stream), sms, kd::wait_limit_ns());
 }
@@ -355,7 +359,7 @@ kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T
   rt.grad_rows = grad_logp;
   rt.kept_logp = kept_logp;
   rt.keep_chunk = kept_logp ? head_fwd_chunk(chunk) : 0;
-  return kd::fused_bwd(h, W, dtype, T, 1, d, V, rt, chunk, temperature, lse, grad_loss, dH, dW,
+  return kd::fused_bwd(h, W, dtype, T, 1, d, V, rt, head_bwd_chunk(chunk), temperature, lse, grad_loss, dH, dW,
                        dW ? dW_dtype : KD_DTYPE_F32, accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
                        kd::wait_limit_ns());
 }

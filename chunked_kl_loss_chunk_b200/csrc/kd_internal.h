@@ -98,6 +98,9 @@ kd_status fused_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t 
 // rows and V = 131072), so a smaller chunk, which bounds the backward's dz, would
 // only cost launches.
 constexpr int64_t KD_HEAD_FWD_ROWS = 2048;
+// Rows that its backward takes at least, of a chunk: those of one GEMM tile, which
+// fewer would leave partly empty.
+constexpr int64_t KD_HEAD_BWD_ROWS = 256;
 
 // The top-K build's workspace: the status word at byte 0 and the row counter
 // (zero before each build) at byte 8.

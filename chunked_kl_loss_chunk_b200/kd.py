@@ -576,6 +576,12 @@ def _head_sizes(h, W, targets):
     return T, d, V, code
 
 
+def _one_group(T: int, chunk: int) -> bool:
+    """Whether the backward forms dz of all T positions at once: two chunks of them,
+    each of at least a GEMM tile's 256 rows."""
+    return T <= 2 * max(chunk, 256)
+
+
 def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, stream=None,
                   backward: bool = False, keep: bool = False):
     """Log-probabilities of one token per position through the output head, the
@@ -584,7 +590,7 @@ def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, 
     ``targets`` int32 [T]; KD_TARGET_IGNORE (-100) marks positions without a
     token (logp 0, no gradient).  ``backward=True`` sizes the workspace for
     ``head_logprobs_bwd`` as well, which takes ``lse`` and may take ``ws``.
-    ``keep=True`` (T <= 2 chunk) leaves in ``ws`` what one backward needs of the
+    ``keep=True`` (T <= 2 chunks, of at least 256 positions each) leaves in ``ws`` what one backward needs of the
     logits, which then does not project again: hand it ``ws`` and
     ``kept_logp=logp``, and let nothing else use ``ws`` in between."""
     use = KD_HEAD_KEEP if keep else (KD_HEAD_BOTH if backward else KD_HEAD_FWD)
@@ -616,7 +622,8 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
     """Gradients of sum_t grad_logp[t] * logp[t] (times the device scalar
     ``grad_loss``): (dH [T, d] dtype of h, dW [V, d] f32, ws).  The logits are
     recomputed chunk by chunk; ``accumulate_dW=True`` adds into a given dW;
-    ``dW_dtype=torch.bfloat16`` gives a bf16 dW where T <= 2 chunk.
+    ``dW_dtype=torch.bfloat16`` gives a bf16 dW where T <= 2 chunks (of at least
+    256 positions each).
     ``need=(dH, dW)`` leaves out a gradient that is not wanted (None in its
     place).  ``kept_logp`` and ``ws`` of a forward with ``keep=True``: its
     exponentials take the place of recomputed logits, and are used up."""
@@ -682,7 +689,7 @@ class HeadLogprobs(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, h, W, targets, chunk, temperature):
-        keep = any(ctx.needs_input_grad[:2]) and h.shape[0] <= 2 * chunk
+        keep = any(ctx.needs_input_grad[:2]) and _one_group(h.shape[0], chunk)
         logp, lse, ws = head_logprobs(h, W, targets, chunk, temperature, keep=keep)
         ctx.save_for_backward(h, W, targets, lse, logp if keep else None)
         ctx.chunk, ctx.temperature = chunk, temperature
@@ -696,7 +703,7 @@ class HeadLogprobs(torch.autograd.Function):
         ws, ctx.ws = ctx.ws, None        # used up: a second backward recomputes
         # dW leaves the kernel in W's type where it is formed in one go, and is added up in fp32
         # and rounded afterwards otherwise
-        direct = h.shape[0] <= 2 * ctx.chunk
+        direct = _one_group(h.shape[0], ctx.chunk)
         dH, dW, _ = head_logprobs_bwd(h, W, targets, lse, g.contiguous(), ctx.chunk, ctx.temperature,
                                       need=ctx.needs_input_grad[:2], ws=ws,
                                       kept_logp=None if ws is None else kept,

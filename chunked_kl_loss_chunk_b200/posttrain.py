@@ -33,7 +33,7 @@ def _through_head(h, W, targets, objective, chunk, temperature, ws, dW, accumula
     flat = targets.reshape(-1)
     # up to two chunks the forward keeps what the backward needs of the logits (a given workspace
     # decides by its size)
-    keep = h.shape[0] <= 2 * chunk
+    keep = kd._one_group(h.shape[0], chunk)
     if keep and ws is not None:
         keep = ws.numel() >= kd.kd_head_logprob_workspace_size(*h.shape, W.shape[0], chunk, kd._dtype_code(h),
                                                                kd.KD_HEAD_KEEP)

@@ -259,7 +259,8 @@ kd_status kd_fused_kl_bwd_shard(const void* h, const void* W, int dtype,
  *   KD_HEAD_BOTH  both calls: as kd_fused_kl_workspace_size (dz of two chunks);
  *   KD_HEAD_KEEP  both calls, the forward keeping what the backward needs of the
  *                 logits in the place of dz: about V / 5 bytes per position more
- *                 than KD_HEAD_BOTH.  T <= 2 chunk (0 otherwise). */
+ *                 than KD_HEAD_BOTH.  T <= 2 chunk (0 otherwise).
+ * Both take at least 256 rows for a chunk (a GEMM tile's), here and below. */
 #define KD_HEAD_FWD 0
 #define KD_HEAD_BOTH 1
 #define KD_HEAD_KEEP 2

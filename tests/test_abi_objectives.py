@@ -39,7 +39,7 @@ def test_head_logprob_refusals(call):
         assert _head(call, **kw) == kd.KD_ERR_UNSUPPORTED, kw
     assert _head(call, ws_bytes=1024) == kd.KD_ERR_WORKSPACE
     # what the forward keeps has to fit one group of two chunks, and its workspace
-    assert _head(call, keep=1, chunk=127) == kd.KD_ERR_UNSUPPORTED
+    assert _head(call, keep=1, T=513) == _head(call, keep=1, T=600, chunk=299) == kd.KD_ERR_UNSUPPORTED
     assert _head(call, keep=1, chunk=128, ws_bytes=kd.kd_head_logprob_workspace_size(256, 256, 4096, 128, 1, 1)) \
         == kd.KD_ERR_WORKSPACE
     if call == "fwd":
@@ -49,7 +49,7 @@ def test_head_logprob_refusals(call):
         assert _head(call, dH=None, dW=None) == kd.KD_ERR_INVALID_ARG
         assert _head(call, gl=FAKE + 2) == kd.KD_ERR_INVALID_ARG
         # a bf16 dW: of bf16 operands, formed in one go, not added to
-        for kw in (dict(dWt=2), dict(dWt=1), dict(dWt=1, chunk=127), dict(dWt=1, chunk=256, acc=1),
+        for kw in (dict(dWt=2), dict(dWt=1, T=513), dict(dWt=1, T=600, chunk=299), dict(dWt=1, chunk=256, acc=1),
                    dict(dWt=1, chunk=256, dtype=kd.KD_DTYPE_F32)):
             assert _head(call, **kw) == kd.KD_ERR_UNSUPPORTED, kw
 
@@ -61,7 +61,9 @@ def test_head_workspace_sizes():
     assert both == kd.kd_fused_kl_workspace_size(2048, 4096, 131072, 1, 2048, kd.KD_DTYPE_BF16)
     assert size(0, 8, 8, 1, 1, 0) == 0
     kept = size(2048, 4096, 131072, 2048, kd.KD_DTYPE_BF16, kd.KD_HEAD_KEEP)
-    assert both < kept <= both + 2048 * 131072 // 4 and size(300, 64, 500, 149, 1, kd.KD_HEAD_KEEP) == 0
+    assert both < kept <= both + 2048 * 131072 // 4 and size(600, 64, 500, 299, 1, kd.KD_HEAD_KEEP) == 0
+    # chunks of less than a tile's rows are taken as 256
+    assert size(512, 64, 500, 1, 1, kd.KD_HEAD_KEEP) == size(512, 64, 500, 256, 1, kd.KD_HEAD_KEEP) > 0
     # the forward's need is refused by the backward, and accepted by the forward's own check
     assert _head("bwd", ws_bytes=kd.kd_head_logprob_workspace_size(256, 256, 4096, 64, 1, 0)) == kd.KD_ERR_WORKSPACE
 

@@ -61,6 +61,7 @@ SHAPES = [
     (129, 64, 257, 4096, torch.bfloat16),
     (5, 4104, 513, 2, torch.bfloat16),
     (600, 128, 2304, 256, torch.float32),
+    (1100, 72, 1003, 300, torch.bfloat16),
     (40, 64, 1, 16, torch.bfloat16),
 ]
 
@@ -83,7 +84,7 @@ def test_forward_and_gradients(T, d, V, chunk, dtype, tau):
     assert bool(((dH.double() - rH).abs() <= 2 * eps * aH + delta * pH + 1e-30).all())
     assert bool(((dW.double() - rW).abs() <= eps * aW + delta * pW + 1e-30).all())
     assert bool((dH[tgt < 0] == 0).all())
-    if T <= 2 * chunk:
+    if T <= 2 * max(chunk, 256):
         # the forward keeps its exponentials: the same logp, one rounding more in dz
         kl, klse, kws = kd.head_logprobs(h, W, tgt, chunk, tau, keep=True)
         assert torch.equal(kl, logp) and torch.equal(klse, lse)
@@ -175,16 +176,16 @@ def test_gradient_against_differences():
 
 def test_autograd_frozen_head_and_accumulation():
     require_gpu()
-    T, d, V = 130, 64, 900
+    T, d, V = 530, 64, 900
     h, W, tgt, g = _inputs(T, d, V, torch.bfloat16, seed=11, ignored=0.0)
     _, lse, _ = kd.head_logprobs(h, W, tgt, 48)
     dH, dW, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, 48)
     hl, Wl = h.clone().requires_grad_(), W.clone().requires_grad_()
-    # (130 positions in chunks of 48 are more than two chunks: recomputed)
+    # (530 positions in chunks of 48, taken as 256, are more than two chunks: recomputed)
     gh, gw = torch.autograd.grad(kd.HeadLogprobs.apply(hl, Wl, tgt, 48, 1.0), (hl, Wl), g)
     assert torch.equal(gh, dH) and torch.equal(gw, dW.to(torch.bfloat16))
     # formed in one go, dW leaves the kernel in bf16: the rounding of the fp32 one
-    for chunk in (65, 130, 1000):
+    for chunk in (265, 530, 1000):
         _, w32, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk)
         _, w16, _ = kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk, dW_dtype=torch.bfloat16)
         assert w16.dtype is torch.bfloat16 and torch.equal(w16, w32.to(torch.bfloat16))
@@ -200,8 +201,8 @@ def test_autograd_frozen_head_and_accumulation():
     with pytest.raises(kd.KDError):
         kd.head_logprobs_bwd(h, W, tgt, lse, g, 64, dW_dtype=torch.bfloat16)
     with torch.no_grad():
-        plain = kd.HeadLogprobs.apply(hl, Wl, tgt, 130)
-    assert not plain.requires_grad and torch.equal(plain, kd.head_logprobs(h, W, tgt, 130)[0])
+        plain = kd.HeadLogprobs.apply(hl, Wl, tgt, 530)
+    assert not plain.requires_grad and torch.equal(plain, kd.head_logprobs(h, W, tgt, 530)[0])
     hf = h.clone().requires_grad_()
     (only,) = torch.autograd.grad(kd.HeadLogprobs.apply(hf, W, tgt, 48, 1.0), (hf,), g)
     assert torch.equal(only, dH)
@@ -267,8 +268,9 @@ def test_refusals():
         kd.head_logprobs_bwd(h, W, tgt, lse, g, 8, need=(False, False))
     with pytest.raises(ValueError):
         kd.head_logprobs_bwd(h, W, tgt, lse, g, 8, kept_logp=lse)
+    h2, W2, tgt2, _ = _inputs(513, 64, 100, torch.bfloat16, seed=1)
     with pytest.raises(kd.KDError):
-        kd.head_logprobs(h, W, tgt, 7, keep=True)                        # more than two chunks
+        kd.head_logprobs(h2, W2, tgt2, 256, keep=True)                   # more than two chunks
     with pytest.raises(kd.KDError):
         kd.head_logprobs(h, W, tgt, 8, keep=True, ws=kd.head_logprobs(h, W, tgt, 8, backward=True)[2])
     with pytest.raises(TypeError):
