@@ -29,6 +29,7 @@ namespace {
 struct {
   decltype(&kd_head_logprob_workspace_size) head_ws;
   decltype(&kd_head_logprob_fwd) head_fwd;
+  decltype(&kd_head_logprob_bwd) head_bwd;
   decltype(&kd_policy_loss_workspace_size) policy_ws;
   decltype(&kd_policy_loss) policy;
   decltype(&kd_preference_loss_workspace_size) preference_ws;
@@ -130,25 +131,26 @@ PyObject* outputs(const T&... t) {
   return r;
 }
 
-// bind(head_ws, head_fwd, policy_ws, policy, preference_ws, preference, clip_ws, clip): addresses
+// bind(addresses of the entry points, in the order of g_lib)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 8) {
-    PyErr_SetString(PyExc_TypeError, "bind: 8 addresses are needed");
+  if (n != 9) {
+    PyErr_SetString(PyExc_TypeError, "bind: 9 addresses are needed");
     return nullptr;
   }
-  void* p[8];
-  for (int i = 0; i < 8; ++i) {
+  void* p[9];
+  for (int i = 0; i < 9; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
   g_lib.head_ws = reinterpret_cast<decltype(g_lib.head_ws)>(p[0]);
   g_lib.head_fwd = reinterpret_cast<decltype(g_lib.head_fwd)>(p[1]);
-  g_lib.policy_ws = reinterpret_cast<decltype(g_lib.policy_ws)>(p[2]);
-  g_lib.policy = reinterpret_cast<decltype(g_lib.policy)>(p[3]);
-  g_lib.preference_ws = reinterpret_cast<decltype(g_lib.preference_ws)>(p[4]);
-  g_lib.preference = reinterpret_cast<decltype(g_lib.preference)>(p[5]);
-  g_lib.clip_ws = reinterpret_cast<decltype(g_lib.clip_ws)>(p[6]);
-  g_lib.clip = reinterpret_cast<decltype(g_lib.clip)>(p[7]);
+  g_lib.head_bwd = reinterpret_cast<decltype(g_lib.head_bwd)>(p[2]);
+  g_lib.policy_ws = reinterpret_cast<decltype(g_lib.policy_ws)>(p[3]);
+  g_lib.policy = reinterpret_cast<decltype(g_lib.policy)>(p[4]);
+  g_lib.preference_ws = reinterpret_cast<decltype(g_lib.preference_ws)>(p[5]);
+  g_lib.preference = reinterpret_cast<decltype(g_lib.preference)>(p[6]);
+  g_lib.clip_ws = reinterpret_cast<decltype(g_lib.clip_ws)>(p[7]);
+  g_lib.clip = reinterpret_cast<decltype(g_lib.clip)>(p[8]);
   Py_RETURN_NONE;
 }
 
@@ -158,39 +160,94 @@ bool bound(Py_ssize_t n, Py_ssize_t want, bool have) {
   return false;
 }
 
+// What both calls of the head take; false for what is not that.
+struct Head {
+  const Tensor *h, *W, *targets, *ws;
+  int64_t T, d, V, chunk;
+  double tau;
+  int dtype;
+};
+bool head_of(PyObject* h, PyObject* W, PyObject* targets, PyObject* chunk, PyObject* tau,
+             PyObject* ws, Head* x) {
+  bool bad = false;
+  x->h = tensor_of(h, &bad);
+  x->W = tensor_of(W, &bad);
+  x->targets = tensor_of(targets, &bad);
+  x->ws = tensor_of(ws, &bad);
+  if (bad || !x->h || !x->W || !x->targets || !PyLong_Check(chunk) || !number(tau, &x->tau))
+    return false;
+  if (!on_current_device(*x->h) || x->h->dim() != 2 || x->W->dim() != 2) return false;
+  x->T = x->h->size(0);
+  x->d = x->h->size(1);
+  x->V = x->W->size(0);
+  const bool bf16 = x->h->scalar_type() == at::kBFloat16;
+  x->dtype = bf16 ? KD_DTYPE_BF16 : KD_DTYPE_F32;
+  int overflow = 0;
+  x->chunk = PyLong_AsLongLongAndOverflow(chunk, &overflow);
+  return !overflow && (bf16 || x->h->scalar_type() == at::kFloat) && x->h->is_contiguous() &&
+         fits(x->W, x->h->scalar_type(), {x->V, x->d}, x->h->device()) &&
+         fits(x->targets, at::kInt, {x->T}, x->h->device()) &&
+         workspace_fits(x->ws, x->h->device());
+}
+
+// The workspace as a tensor to hand on.
+Tensor given_out(const Tensor* ws, const Workspace& w) {
+  return ws ? *ws
+            : w.own.narrow(0, static_cast<char*>(w.at) - static_cast<char*>(w.own.data_ptr()),
+                           static_cast<int64_t>(w.bytes));
+}
+
 // head_logprobs(h, W, targets, chunk, temperature, use, ws)
 PyObject* head_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!bound(n, 7, g_lib.head_fwd)) return nullptr;
-  bool bad = false;
-  const Tensor *h = tensor_of(a[0], &bad), *W = tensor_of(a[1], &bad);
-  const Tensor *targets = tensor_of(a[2], &bad), *ws = tensor_of(a[6], &bad);
-  double tau;
-  if (bad || !h || !W || !targets || !PyLong_Check(a[3]) || !number(a[4], &tau)) Py_RETURN_NONE;
-  if (!on_current_device(*h) || h->dim() != 2 || W->dim() != 2) Py_RETURN_NONE;
-  const int64_t T = h->size(0), d = h->size(1), V = W->size(0);
-  const bool bf16 = h->scalar_type() == at::kBFloat16;
-  if ((!bf16 && h->scalar_type() != at::kFloat) || !h->is_contiguous() ||
-      !fits(W, h->scalar_type(), {V, d}, h->device()) ||
-      !fits(targets, at::kInt, {T}, h->device()) || !workspace_fits(ws, h->device()))
-    Py_RETURN_NONE;
-  const int64_t chunk = PyLong_AsLongLong(a[3]);
+  Head x;
+  if (!head_of(a[0], a[1], a[2], a[3], a[4], a[6], &x)) Py_RETURN_NONE;
   const int use = static_cast<int>(PyLong_AsLong(a[5]));
   if (PyErr_Occurred()) return nullptr;
-  const int dtype = bf16 ? KD_DTYPE_BF16 : KD_DTYPE_F32;
-  Workspace w(ws, ws ? 0 : g_lib.head_ws(T, d, V, chunk, dtype, use), *h);
-  const auto f32 = h->options().dtype(at::kFloat);
-  Tensor logp = at::empty({T}, f32), lse = at::empty({T}, f32);
+  Workspace w(x.ws, x.ws ? 0 : g_lib.head_ws(x.T, x.d, x.V, x.chunk, x.dtype, use), *x.h);
+  const auto f32 = x.h->options().dtype(at::kFloat);
+  Tensor logp = at::empty({x.T}, f32), lse = at::empty({x.T}, f32);
   const kd_status st = g_lib.head_fwd(
-      h->data_ptr(), W->data_ptr(), dtype, T, d, V, data<const int32_t>(targets), chunk,
-      static_cast<float>(tau), use == KD_HEAD_KEEP, logp.data_ptr<float>(), lse.data_ptr<float>(),
-      w.at, w.bytes, current_stream(*h));
+      x.h->data_ptr(), x.W->data_ptr(), x.dtype, x.T, x.d, x.V, data<const int32_t>(x.targets),
+      x.chunk, static_cast<float>(x.tau), use == KD_HEAD_KEEP, logp.data_ptr<float>(),
+      lse.data_ptr<float>(), w.at, w.bytes, current_stream(*x.h));
   if (st != KD_OK) return PyLong_FromLong(st);
-  const Tensor given = ws ? *ws
-                          : w.own.narrow(0, static_cast<char*>(w.at) -
-                                                static_cast<char*>(w.own.data_ptr()),
-                                         static_cast<int64_t>(w.bytes));
-  return outputs(logp, lse, given);
+  return outputs(logp, lse, given_out(x.ws, w));
+  END_HANDLE_TH_ERRORS
+}
+
+// head_logprobs_bwd(h, W, targets, lse, kept_logp, grad_logp, grad_loss, chunk, temperature,
+//                   need dH, need dW, dW in bf16, ws): new dH and dW
+PyObject* head_logprobs_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!bound(n, 13, g_lib.head_bwd)) return nullptr;
+  Head x;
+  bool bad = false;
+  const Tensor *lse = tensor_of(a[3], &bad), *kept = tensor_of(a[4], &bad);
+  const Tensor *grad = tensor_of(a[5], &bad), *grad_loss = tensor_of(a[6], &bad);
+  if (bad || !lse || !grad || !head_of(a[0], a[1], a[2], a[7], a[8], a[12], &x) ||
+      (kept && !x.ws))
+    Py_RETURN_NONE;
+  const auto dev = x.h->device();
+  if (!fits(lse, at::kFloat, {x.T}, dev) || !fits(kept, at::kFloat, {x.T}, dev) ||
+      !fits(grad, at::kFloat, {x.T}, dev) ||
+      (grad_loss && (grad_loss->numel() != 1 || !fits(grad_loss, at::kFloat, grad_loss->sizes(), dev))))
+    Py_RETURN_NONE;
+  const bool need_h = PyObject_IsTrue(a[9]), need_w = PyObject_IsTrue(a[10]);
+  const bool w_bf16 = PyObject_IsTrue(a[11]);
+  Workspace w(x.ws, x.ws ? 0 : g_lib.head_ws(x.T, x.d, x.V, x.chunk, x.dtype, KD_HEAD_BOTH), *x.h);
+  Tensor dH, dW;
+  if (need_h) dH = at::empty({x.T, x.d}, x.h->options());
+  if (need_w) dW = at::empty({x.V, x.d}, x.h->options().dtype(w_bf16 ? at::kBFloat16 : at::kFloat));
+  const kd_status st = g_lib.head_bwd(
+      x.h->data_ptr(), x.W->data_ptr(), x.dtype, x.T, x.d, x.V, data<const int32_t>(x.targets),
+      x.chunk, static_cast<float>(x.tau), data<const float>(lse), data<const float>(kept),
+      data<const float>(grad), data<const float>(grad_loss), need_h ? dH.data_ptr() : nullptr,
+      need_w ? dW.data_ptr() : nullptr, w_bf16 ? KD_DTYPE_BF16 : KD_DTYPE_F32, 0, w.at, w.bytes,
+      current_stream(*x.h));
+  if (st != KD_OK) return PyLong_FromLong(st);
+  return outputs(dH, dW, given_out(x.ws, w));
   END_HANDLE_TH_ERRORS
 }
 
@@ -332,6 +389,7 @@ PyMethodDef method(const char* name, Fast f) {
 
 PyMethodDef g_methods[] = {method("bind", bind),
                            method("head_logprobs", head_logprobs),
+                           method("head_logprobs_bwd", head_logprobs_bwd),
                            method("policy_loss", policy_loss),
                            method("preference_loss", preference_loss),
                            method("clip_grad_norm", clip_grad_norm),

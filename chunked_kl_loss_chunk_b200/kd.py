@@ -104,7 +104,7 @@ GEMM_KIND_NAMES = {1: "fwd_lse", 2: "bwd_dz", 4: "dH", 8: "dW", 12: "dH+dW"}
 _lib = None
 _native = None
 # the entry points that _kd_native calls, in the order of its bind()
-_NATIVE_CALLS = ("kd_head_logprob_workspace_size", "kd_head_logprob_fwd",
+_NATIVE_CALLS = ("kd_head_logprob_workspace_size", "kd_head_logprob_fwd", "kd_head_logprob_bwd",
                  "kd_policy_loss_workspace_size", "kd_policy_loss",
                  "kd_preference_loss_workspace_size", "kd_preference_loss",
                  "kd_grad_clip_workspace_size", "kd_grad_clip")
@@ -627,6 +627,13 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
     ``need=(dH, dW)`` leaves out a gradient that is not wanted (None in its
     place).  ``kept_logp`` and ``ws`` of a forward with ``keep=True``: its
     exponentials take the place of recomputed logits, and are used up."""
+    load()
+    if stream is None and dH is None and dW is None and not accumulate_dW and any(need) and \
+            (dW_dtype is torch.float32 or dW_dtype is torch.bfloat16):
+        out = _native.head_logprobs_bwd(h, W, targets, lse, kept_logp, grad_logp, grad_loss, chunk, temperature,
+                                        need[0], need[1], dW_dtype is torch.bfloat16, ws)
+        if out is not None:
+            return _native_result(out, "kd_head_logprob_bwd")
     T, d, V, code = _head_sizes(h, W, targets)
     _require("lse", lse, torch.float32, (T,), h.device)
     _require("grad_logp", grad_logp, torch.float32, (T,), h.device)

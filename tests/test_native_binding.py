@@ -20,6 +20,7 @@ def test_none_for_what_is_not_on_a_gpu():
     assert n.policy_loss(x, x, None, a, False, None, None, 0.2, 0.2, 0.0, 0, 0.0, True, None) is None
     assert n.preference_loss(x, None, None, None, 0, 0.1, 0.0, 0.0, False, None, True, None) is None
     assert n.head_logprobs(x, x, a.int(), 4, 1.0, 0, None) is None
+    assert n.head_logprobs_bwd(x, x, a.int(), a, None, a, None, 4, 1.0, True, True, False, None) is None
     assert n.clip_grad_norm([x, a], None, 1.0, None) is None
     assert n.clip_grad_norm([], None, 1.0, None) is None
 
@@ -40,7 +41,8 @@ def test_none_for_what_is_no_tensor(bad):
 
 
 def test_wrong_number_of_arguments():
-    for f in (kd._native.policy_loss, kd._native.preference_loss, kd._native.head_logprobs, kd._native.clip_grad_norm):
+    n = kd._native
+    for f in (n.policy_loss, n.preference_loss, n.head_logprobs, n.head_logprobs_bwd, n.clip_grad_norm):
         with pytest.raises(TypeError):
             f(1, 2)
     with pytest.raises(TypeError):
