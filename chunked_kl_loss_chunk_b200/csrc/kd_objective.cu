@@ -284,8 +284,9 @@ __device__ __forceinline__ F2 exp2v(const F2& x) {
 // k = e^q - 1 - q without the cancellation of small q: q^2 times the Taylor series
 // of (e^q - 1 - q) / q^2, whose first left-out term is below 2^-20 of it for
 // |q| < 1/2.  Both forms are computed: a warp's tokens would take both branches as
-// a rule.
-__device__ __forceinline__ F2 exp_minus_linear(const F2& q) {
+// a rule.  em1: e^q - 1, which for a large -q (or an infinite one: the reference holds
+// the token impossible) is not to be had as k + q any more.
+__device__ __forceinline__ F2 exp_minus_linear(const F2& q, F2& em1) {
   F2 s = f2(1.f / 5040.f);
   s = fma2(s, q, f2(1.f / 720.f));
   s = fma2(s, q, f2(1.f / 120.f));
@@ -293,12 +294,16 @@ __device__ __forceinline__ F2 exp_minus_linear(const F2& q) {
   s = fma2(s, q, f2(1.f / 6.f));
   s = fma2(s, q, f2(0.5f));
   s = mul2(mul2(q, q), s);
-  const F2 far = fma2(q, f2(-1.f), add2(exp2v(q), f2(-1.f)));
-  float q0, q1, s0, s1, f0, f1;
+  const F2 far1 = add2(exp2v(q), f2(-1.f)), far = fma2(q, f2(-1.f), far1);
+  float q0, q1, s0, s1, f0, f1, m0, m1, g0, g1;
   f2_get(q, q0, q1);
   f2_get(s, s0, s1);
   f2_get(far, f0, f1);
-  return f2(fabsf(q0) < 0.5f ? s0 : f0, fabsf(q1) < 0.5f ? s1 : f1);
+  f2_get(add2(s, q), m0, m1);
+  f2_get(far1, g0, g1);
+  const bool near0 = fabsf(q0) < 0.5f, near1 = fabsf(q1) < 0.5f;
+  em1 = f2(near0 ? m0 : g0, near1 ? m1 : g1);
+  return f2(near0 ? s0 : f0, near1 ? s1 : f1);
 }
 
 // Which of the 16 tokens from t0 the mask keeps, as bits.
@@ -548,16 +553,16 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
         }
         // r against the border in the logarithm.  d is the rounded difference, and rounding
         // keeps order: only d equal to the rounded border needs the exact difference.
-        // (For A < 0 both sides are negated.)
+        // (For A < 0 both sides are negated; an A of 0 or NaN is not clipped.)
         const bool up0 = A0 > 0.f, up1 = A1 > 0.f;
         const float border0 = up0 ? a.log_hi : -a.log_lo, border1 = up1 ? a.log_hi : -a.log_lo;
         const float e0 = up0 ? d0 : -d0, e1 = up1 ? d1 : -d1;
-        bool clip0 = e0 > border0 && A0 != 0.f, clip1 = e1 > border1 && A1 != 0.f;
+        bool clip0 = e0 > border0 && fabsf(A0) > 0.f, clip1 = e1 > border1 && fabsf(A1) > 0.f;
         if (e0 == border0 || e1 == border1) {
           const double x0 = OLD && on0 ? static_cast<double>(lp[j]) - od[j] : 0.0;
           const double x1 = OLD && on1 ? static_cast<double>(lp[j + 1]) - od[j + 1] : 0.0;
-          clip0 = A0 != 0.f && (up0 ? x0 > a.log_hi64 : x0 < a.log_lo64);
-          clip1 = A1 != 0.f && (up1 ? x1 > a.log_hi64 : x1 < a.log_lo64);
+          clip0 = fabsf(A0) > 0.f && (up0 ? x0 > a.log_hi64 : x0 < a.log_lo64);
+          clip1 = fabsf(A1) > 0.f && (up1 ? x1 > a.log_hi64 : x1 < a.log_lo64);
         }
         float r0, r1, t0_, t1_;
         f2_get(ratio, r0, r1);
@@ -570,11 +575,12 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
           float x0, x1;
           f2_get(add2(f2(rf[j], rf[j + 1]), nlp), x0, x1);
           const F2 x = f2(on0 ? x0 : 0.f, on1 ? x1 : 0.f);
-          const F2 k = exp_minus_linear(x);
+          F2 em1;
+          const F2 k = exp_minus_linear(x, em1);
           s_kl = add2(s_kl, k);
           if (a.kl_coef != 0.f) {                      // 0 times an infinite k stays out
             term = fma2(f2(-a.kl_coef), k, term);
-            grad = fma2(f2(a.kl_coef), add2(k, x), grad);       // 1 - e^x = -(k + x)
+            grad = fma2(f2(a.kl_coef), em1, grad);
           }
         }
         const F2 nw = f2(-wt[j], -wt[j + 1]);
@@ -717,8 +723,9 @@ __global__ void __launch_bounds__(OBJ_THREADS, 1) policy_one_kernel(const Policy
 //   z = beta D - margin
 //   sigmoid  -(1 - e) log s(z) - e log s(-z);  hinge  max(0, 1 - z);
 //   ipo      (D - 1 / (2 beta))^2
-// Three steps: sums over every sequence; one warp for each pair; the gradient,
-// one value per sequence, spread over its tokens.
+// Three steps: sums over every sequence; the pairs, a warp each or, where there are
+// more of them than warps, a lane; the gradient, one value per sequence, spread over
+// its tokens.
 //
 // The sums.  A warp walks a span of tokens, 128 at a time, adding each lane's
 // four tokens in fp64 (a sum of 100,000 log-probabilities would lose 1e-2 of a
@@ -949,7 +956,8 @@ __device__ __forceinline__ double pref_pair(const PrefArgs& a, int32_t i, int la
     slope = z < 1.0 ? -a.beta : (z >= 1.0 ? 0.0 : z);
   } else {
     const double soft = log1p(exp(-fabs(z)));
-    loss = (1.0 - a.smoothing) * (fmax(-z, 0.0) + soft) + a.smoothing * (fmax(z, 0.0) + soft);
+    loss = (1.0 - a.smoothing) * (fmax(-z, 0.0) + soft);
+    if (a.smoothing > 0.0) loss += a.smoothing * (fmax(z, 0.0) + soft);   // z may be infinite
     if (z != z) loss = z;
     slope = a.beta * (a.smoothing - 1.0 / (1.0 + exp(z)));
   }

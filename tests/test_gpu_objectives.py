@@ -134,6 +134,48 @@ def test_policy_loss(name, masked):
         assert torch.equal(kd.policy_loss(x["logp"], old, adv, **kw)[2], g)
 
 
+@pytest.mark.parametrize("n", [5, 5000])
+def test_a_reference_that_holds_tokens_impossible(n):
+    """ref_logp very low or -inf: the KL term grows without bound, its gradient is beta (1 - e^q)
+    all the same, here w beta to one rounding each of beta, 1 - e^q and the product
+    (e^q < 2^-24), and of the weight: 2^-22."""
+    require_gpu()
+    low = [-np.inf, float(np.finfo(np.float32).min), -1e9, -1e5, -3000.0, -200.0, -40.0]
+    logp = torch.full((n, 1), -0.5, device="cuda")
+    ref = torch.tensor([low[i % len(low)] for i in range(n)], device="cuda").reshape(n, 1)
+    loss, stats, g = kd.policy_loss(logp, None, torch.zeros(n, device="cuda"), ref_logp=ref, kl_coef=0.25,
+                                    reduction="fixed", denom=8.0)
+    assert loss.item() == np.inf and stats[3].item() == np.inf
+    assert torch.all((g.double() - 0.25 / 8).abs() <= 2.0 ** -22 * 0.25 / 8)
+
+
+@pytest.mark.parametrize("n", [4, 4000])
+def test_a_nan_advantage_is_not_clipped(n):
+    """The clamp belongs to advantages above and below 0: a NaN reaches loss and gradient, as the
+    formula says, and only its own token's."""
+    require_gpu()
+    logp = torch.full((n, 1), -1.0, device="cuda")
+    old = logp + 2.0 * (1 - 2 * (torch.arange(n, device="cuda") % 2)).reshape(n, 1)      # r = e^-2, e^2
+    adv = torch.where(torch.arange(n, device="cuda") < n // 2, torch.nan, 0.0)
+    loss, stats, g = kd.policy_loss(logp, old, adv)
+    assert torch.isnan(loss) and stats[2].item() == 0
+    assert torch.equal(torch.isnan(g).flatten(), torch.isnan(adv)) and torch.all(g[n // 2:] == 0)
+
+
+@pytest.mark.parametrize("pairs", [1, 700])
+def test_an_impossible_rejected_answer(pairs):
+    """z = +inf: -log sigmoid(z) is 0, and so are the slope and, without label smoothing, the loss;
+    with it the loss is infinite."""
+    require_gpu()
+    logp = torch.full((2 * pairs, 2), -1.0, device="cuda")
+    logp[pairs:, 1] = -torch.inf
+    loss, rewards, g = kd.preference_loss(logp)
+    assert loss.item() == 0 and torch.all(g == 0) and torch.all(rewards[pairs:] == -torch.inf)
+    loss, _, g = kd.preference_loss(logp, label_smoothing=0.25, beta=0.5)
+    assert loss.item() == np.inf
+    assert torch.all(((g[:pairs].double() * pairs) - 0.125).abs() <= 2.0 ** -22)
+
+
 def test_clipping_is_decided_as_in_exact_arithmetic():
     """Ratios within a few roundings of the borders, both signs of the advantage."""
     require_gpu()
