@@ -408,13 +408,17 @@ kd_status kd_policy_loss(const float* logp, const float* old_logp, const float* 
       !aligned(advantages, 4) || !aligned(loss, 4) || !aligned(stats, 4) || !aligned(dlogp, 4) ||
       !aligned(ws, 1024))
     return KD_ERR_INVALID_ARG;
-  if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0) || !isfinite(kl_coef) ||
+  if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0) ||
+      !isfinite(static_cast<float>(kl_coef)) ||
       (kl_coef != 0.0 && !ref_logp))
     return KD_ERR_INVALID_ARG;
   if (reduction != KD_REDUCE_TOKEN && reduction != KD_REDUCE_SEQUENCE &&
       reduction != KD_REDUCE_FIXED)
     return KD_ERR_INVALID_ARG;
-  if (reduction == KD_REDUCE_FIXED && !(denom > 0.0 && isfinite(denom))) return KD_ERR_INVALID_ARG;
+  // (an infinite weight would make the zeros of tokens that do not count NaN)
+  if (reduction == KD_REDUCE_FIXED &&
+      !(denom > 0.0 && isfinite(denom) && isfinite(static_cast<float>(1.0 / denom))))
+    return KD_ERR_INVALID_ARG;
   kd::PolicyArgs a = {};
   const kd_status st = validate_layout(cu_seqlens, n_seqs, n_tokens, &a.seq);
   if (st != KD_OK) return st;

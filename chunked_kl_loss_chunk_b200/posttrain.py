@@ -29,7 +29,10 @@ class Step(NamedTuple):
     ws: torch.Tensor          # the head's workspace, for kd.read_device_status or the next step
 
 
-def _through_head(h, W, targets, objective, chunk, temperature, ws, dW, accumulate_dW):
+def _through_head(h, W, targets, objective, options, chunk, temperature, ws, dW, accumulate_dW):
+    for name in ("grad", "stream"):        # the step needs the gradient, and all of it on one stream
+        if name in options:
+            raise TypeError(f"{name}: not an option of a step")
     flat = targets.reshape(-1)
     # up to two chunks the forward keeps what the backward needs of the logits (a given workspace
     # decides by its size)
@@ -58,7 +61,7 @@ def policy_step(h, W, targets, old_logp, advantages, *, chunk: int, temperature:
     token count and ``accumulate_dW=True`` add up to the batch's gradient."""
     return _through_head(h, W, targets, lambda logp, mask: kd.policy_loss(
         logp, old_logp, advantages, mask=mask, ref_logp=ref_logp, cu_seqlens=cu_seqlens, **options),
-        chunk, temperature, ws, dW, accumulate_dW)
+        options, chunk, temperature, ws, dW, accumulate_dW)
 
 
 def preference_step(h, W, targets, *, chunk: int, temperature: float = 1.0, ref_logp=None, cu_seqlens=None,
@@ -70,4 +73,4 @@ def preference_step(h, W, targets, *, chunk: int, temperature: float = 1.0, ref_
     (kind, beta, margin, label_smoothing, length_normalize, pairs_total)."""
     return _through_head(h, W, targets, lambda logp, mask: kd.preference_loss(
         logp, ref_logp=ref_logp, mask=mask, cu_seqlens=cu_seqlens, **options),
-        chunk, temperature, ws, dW, accumulate_dW)
+        options, chunk, temperature, ws, dW, accumulate_dW)

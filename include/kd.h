@@ -348,7 +348,8 @@ size_t kd_policy_loss_workspace_size(int64_t n_seqs, int64_t n_tokens);
  *   old_logp    of the policy that sampled; NULL: logp itself, so r = 1
  *   ref_logp    of the reference; NULL: no KL (kl_coef must then be 0)
  *   advantages  [n_tokens] if advantages_per_token != 0, else [n_seqs]
- *   clip_low in [0, 1], clip_high >= 0; denom > 0 for KD_REDUCE_FIXED only
+ *   clip_low in [0, 1], clip_high >= 0; denom > 0 for KD_REDUCE_FIXED only; kl_coef
+ *   and 1 / denom within float32's range
  * Outputs (device): loss float32 scalar; stats float32 [4]: the number of
  * tokens that count, and over them the means of r, of "clipped" (r A above its
  * clamped value) and of exp(q) - 1 - q; dlogp float32 [n_tokens], or NULL.

@@ -54,6 +54,23 @@ def test_head_logprob_refusals(call):
             assert _head(call, **kw) == kd.KD_ERR_UNSUPPORTED, kw
 
 
+def test_policy_factors_beyond_fp32():
+    """kl_coef and 1 / denom are used in fp32: an infinite one would turn zeros into NaN."""
+    for kw in (dict(kl=1e39), dict(kl=-1e39), dict(red=2, denom=1e-39), dict(red=2, denom=5e-324)):
+        assert _policy(**kw) == kd.KD_ERR_INVALID_ARG, kw
+
+
+@pytest.mark.parametrize("name", ["grad", "stream"])
+def test_step_options(name):
+    """A step needs the objective's gradient, and the objective on the step's stream."""
+    from chunked_kl_loss_chunk_b200 import posttrain
+    h, W, targets = torch.zeros(4, 8), torch.zeros(16, 8), torch.zeros(2, 2, dtype=torch.int32)
+    with pytest.raises(TypeError, match=name):
+        posttrain.policy_step(h, W, targets, None, torch.zeros(2), chunk=4, **{name: None})
+    with pytest.raises(TypeError, match=name):
+        posttrain.preference_step(h, W, targets, chunk=4, **{name: None})
+
+
 def test_head_workspace_sizes():
     size = kd.kd_head_logprob_workspace_size
     fwd, both = (size(2048, 4096, 131072, 2048, kd.KD_DTYPE_BF16, b) for b in (0, 1))
