@@ -11,6 +11,7 @@
 // in kd_gemm2.cuh.
 #pragma once
 
+#include "kd_boxes.h"
 #include "kd_common.cuh"
 
 namespace kd {
@@ -22,7 +23,7 @@ constexpr int ROW_BYTES = 128;                 // K depth of a stage, in bytes
 constexpr int TMEM_COLS = 2 * BN;              // two accumulators
 constexpr int EPI_WARPS = 4;
 constexpr int EPI_BUF_BYTES = 32 * 128;        // one 32x32 fp32 (or 32x32 bf16) output box
-constexpr int EPI_SMEM_BYTES = EPI_WARPS * 2 * EPI_BUF_BYTES;   // double-buffered per warp
+constexpr int EPI_SMEM_BYTES = EPI_WARPS * EPI_BOXES * EPI_BUF_BYTES;
 
 template <typename Elem>
 struct ElemCfg;
@@ -129,9 +130,9 @@ __device__ __forceinline__ void emit_box(const CUtensorMap* tmC, unsigned char* 
   }
 }
 
-// Before reusing a box: the transfer issued from it two blocks ago has read it.
+// Before reusing a box: the transfer issued from it two boxes ago has read it.
 __device__ __forceinline__ void box_reuse_wait() {
-  if ((threadIdx.x & 31) == 0) bulk_wait_read<1>();
+  if ((threadIdx.x & 31) == 0) bulk_wait_read<BOX_READS_PENDING>();
   __syncwarp();
 }
 
@@ -148,15 +149,17 @@ __device__ __forceinline__ int lower_bound_i32(const int32_t* ids, int K, int32_
 // ----------------------------------------------------------------------------
 // Epilogues.  Called by the 128 epilogue threads; `taddr` addresses this
 // warp's 32 TMEM lanes at the tile's first accumulator column; `boxes` is the
-// warp's pair of output boxes.  Every lane of a warp executes the same sequence
-// of tcgen05.ld (they are warp-collective).
+// warp's pair of output boxes and `turn` the number it has taken of them, over all of
+// its tiles.  Every lane of a warp executes the same sequence of tcgen05.ld (they
+// are warp-collective).
 // ----------------------------------------------------------------------------
 template <typename Elem, int EPI>
 // pace_ns (dW): pause between two output boxes of a warp, so that a
 // tile's dW boxes go out spread over the next tile's mainloop.
 __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMap* tmC, int m_base,
                                              int nb, uint32_t taddr, int quad, int lane,
-                                             unsigned char* boxes, int y_extra = 0,
+                                             unsigned char* boxes, uint32_t& turn,
+                                             int y_extra = 0,
                                              uint32_t pace_ns = 0) {
   const int r = quad * 32 + lane;         // accumulator row of this thread
   const int m = m_base + r;               // output row within the problem
@@ -223,7 +226,7 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
           }
           if (row_ok) g.block_max[static_cast<int64_t>(base / 32) * g.ld_max + t] = nm;
-          unsigned char* box = boxes + (c & 1) * EPI_BUF_BYTES;
+          unsigned char* box = boxes + box_take(turn) * EPI_BUF_BYTES;
           box_reuse_wait();
           if constexpr (sizeof(Elem) == 4) stage_box_f32(box, lane, v);
           else stage_box_bf16(box, lane, v);
@@ -246,7 +249,7 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
       for (int c = 0; c < BN / 32; ++c) {
         const int base = n0 + c * 32;
         if (base >= g.V) break;
-        unsigned char* box = boxes + (c & 1) * EPI_BUF_BYTES;
+        unsigned char* box = boxes + box_take(turn) * EPI_BUF_BYTES;
         box_reuse_wait();
         float v[32];
         tmem_ld32(taddr + c * 32, v);
@@ -274,7 +277,7 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
     for (int c = 0; c < BN / 32; ++c) {
       const int base = n0 + c * 32;
       if (base >= g.N) break;
-      unsigned char* box = boxes + (c & 1) * EPI_BUF_BYTES;
+      unsigned char* box = boxes + box_take(turn) * EPI_BUF_BYTES;
       box_reuse_wait();
       float v[32];
       tmem_ld32(taddr + c * 32, v);

@@ -333,7 +333,8 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     // ------------------------------------------------------------ epilogue (both CTAs)
     griddep_wait();
     const int quad = warp & 3;
-    unsigned char* boxes = sEpi + (warp - 2) * 2 * EPI_BUF_BYTES;
+    unsigned char* boxes = sEpi + (warp - 2) * EPI_BOXES * EPI_BUF_BYTES;
+    uint32_t turn = 0;                           // boxes taken, over all tiles
     const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty[1]), 0);
     int acc = 0;
@@ -368,7 +369,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                              static_cast<uint32_t>(acc * BN);
       run_epilogue<Elem, EPI>(g, &tmC, w.mb2 * BM2 + static_cast<int>(rank) * 128, w.nb, taddr,
-                              quad, lane, boxes, w.split * g.split_rows, pace_ns);
+                              quad, lane, boxes, turn, w.split * g.split_rows, pace_ns);
       __syncwarp();
       tc_fence_before();
       if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
