@@ -95,10 +95,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
   return ok != 0;
 }
 
+// A wait that ran out, in the place of a bad index that may be recorded already:
+// the other waits have to see it.
+__device__ __forceinline__ void set_timeout(uint32_t* status) {
+  if (atomicCAS(status, 0u, KD_ERR_TIMEOUT) == KD_ERR_BAD_INDEX)
+    atomicCAS(status, static_cast<uint32_t>(KD_ERR_BAD_INDEX), static_cast<uint32_t>(KD_ERR_TIMEOUT));
+}
+
 // Wait until the phase with the given parity has completed.  Gives up after
-// `limit_ns` of wall time, or as soon as another thread of the grid has
-// recorded an error, recording KD_ERR_TIMEOUT in the first case.  Returns true
-// on success.
+// `limit_ns` of wall time, recording KD_ERR_TIMEOUT, or as soon as another thread
+// of the call has recorded that or a broken invariant.  (A bad index is an error of
+// its row alone; the other rows are worked on to the end.)  Returns true on success.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                           uint32_t* status) {
   const uint32_t a = smem_u32(bar);
@@ -107,9 +114,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(a, parity)) return true;
     if ((it & 63u) == 0u) {
-      if (read_status(status) != 0u) return false;
+      const uint32_t code = read_status(status);
+      if (code != 0u && code != KD_ERR_BAD_INDEX) return false;
       if (globaltimer_ns() - t0 > limit_ns) {
-        set_status(status, KD_ERR_TIMEOUT);
+        set_timeout(status);
         return false;
       }
     }
