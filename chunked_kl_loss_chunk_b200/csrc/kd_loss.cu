@@ -258,8 +258,10 @@ prep_reg_kernel(const float* __restrict__ vals, const int32_t* __restrict__ idx,
 //   coef (S softmax - p [v == y])  is  g_t / tau ([v == y] - softmax),
 // the gradient of g_t logp_t.  A row whose target is KD_TARGET_IGNORE gets
 // p = S = 0 and an index past V (its g_t is not read); any other target outside
-// [0, V) gets the same and records KD_ERR_BAD_INDEX.  A single block also clears the
-// status word, in the place of a memset before it (2 us of a short call).
+// [0, V) gets the same and records KD_ERR_BAD_INDEX.  The second statistic is the
+// log-probability of a row without an entry: 0, or NaN for a bad target, so that it
+// does not go unnoticed where nobody reads the status.  A single block also clears
+// the status word, in the place of a memset before it (2 us of a short call).
 constexpr int64_t PREP_ONE_BLOCK = 4096;      // rows
 __global__ void __launch_bounds__(1024)
 prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict__ grad, int64_t T,
@@ -277,8 +279,9 @@ prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict_
     const float p = !ok ? 0.f : (grad ? -grad[t] : 1.f);
     idx_sorted[t] = ok ? y : INT32_MAX;
     p_sorted[t] = p;
-    stats[t] = make_float2(p, 0.f);
-    if (!ok && y != KD_TARGET_IGNORE) set_status(status, KD_ERR_BAD_INDEX);
+    const bool bad = !ok && y != KD_TARGET_IGNORE;
+    stats[t] = make_float2(p, bad ? __int_as_float(0x7FC00000) : 0.f);
+    if (bad) set_status(status, KD_ERR_BAD_INDEX);
   }
 }
 
@@ -287,7 +290,7 @@ prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict_
 // row; lane l merges tiles l, l+32, ... in order, then a fixed shuffle tree.
 //   LSE_t = M/tau + ln S,  KL_t = sum p log p - G/tau + (sum p) LSE_t
 // or, with LOGP (one target per row, p = 1 at it):
-//   logp_t = G/tau - LSE_t, and 0 for a row without a target (p = 0).
+//   logp_t = G/tau - LSE_t, and the second statistic for a row without a target (p = 0).
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void merge_lse(float& m, float& s, float m2, float s2, float zs) {
   const float nm = fmaxf(m, m2);
@@ -336,7 +339,7 @@ combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64
     const float L = m * inv_tau + logf(s);
     const float2 st = stats[t];
     lse[t] = L;
-    if constexpr (LOGP) kl[t] = st.x != 0.f ? gsum * inv_tau - L : 0.f;
+    if constexpr (LOGP) kl[t] = st.x != 0.f ? gsum * inv_tau - L : st.y;
     else kl[t] = st.y - gsum * inv_tau + st.x * L;
   }
 }

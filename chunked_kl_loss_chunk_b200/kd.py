@@ -588,7 +588,8 @@ def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, 
     [T, V] logits never materialised: (logp f32 [T], lse f32 [T], ws).
 
     ``targets`` int32 [T]; KD_TARGET_IGNORE (-100) marks positions without a
-    token (logp 0, no gradient).  ``backward=True`` sizes the workspace for
+    token (logp 0, no gradient).  Any other target outside [0, V) gives a logp of
+    NaN and no gradient, and KD_ERR_BAD_INDEX in ``ws``.  ``backward=True`` sizes the workspace for
     ``head_logprobs_bwd`` as well, which takes ``lse`` and may take ``ws``.
     ``keep=True`` (T <= 2 chunks, of at least 256 positions each) leaves in ``ws`` what one backward needs of the
     logits, which then does not project again: hand it ``ws`` and
@@ -682,8 +683,8 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
 
 class HeadLogprobs(torch.autograd.Function):
     """``logp = HeadLogprobs.apply(h, W, targets, chunk, temperature=1.0)``: the
-    log-probabilities of ``head_logprobs`` with gradients to h and W (W's in
-    W's dtype).  Up to two chunks of positions the forward keeps what the
+    log-probabilities of ``head_logprobs`` (NaN for a target that is neither a token
+    nor KD_TARGET_IGNORE) with gradients to h and W (W's in W's dtype).  Up to two chunks of positions the forward keeps what the
     backward needs of the logits (2 V bytes per position for bf16, in the
     workspace that the backward needs anyway); beyond, the backward recomputes
     them chunk by chunk."""

@@ -277,8 +277,8 @@ size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t c
  * leaves the exponentials of the logits in ws, in the operands' type, for ONE
  * kd_head_logprob_bwd on the same ws, inputs and sizes: it then need not project
  * again.  Nothing else may use ws in between.  A target outside [0, V)
- * other than KD_TARGET_IGNORE is recorded as KD_ERR_BAD_INDEX; the outputs of
- * that call are then unspecified.
+ * other than KD_TARGET_IGNORE is recorded as KD_ERR_BAD_INDEX, and the logp of its
+ * row is NaN; the other rows are as ever.
  */
 kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
@@ -297,6 +297,7 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
  * kept_logp: the logp of the forward that kept its exponentials in this ws, which
  * this call uses up; NULL: the logits are recomputed.  The kept ones are rounded
  * once more (each dz entry but the target's has two roundings in place of one).
+ * A row with a bad target (recorded as KD_ERR_BAD_INDEX) adds nothing to either.
  * Either of dH and dW may be NULL: that gradient is not computed (a frozen head
  * needs no dW).  dz is rounded to the operands' type, as in kd_fused_kl_bwd.  An ignored row
  * contributes 0 times its h to dW, so h must be finite in every row.
