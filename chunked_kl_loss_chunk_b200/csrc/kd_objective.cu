@@ -116,15 +116,31 @@ __device__ __forceinline__ void row_sequences(const SeqLayout& q, const Cursor& 
   }
 }
 
-// Records KD_ERR_BAD_INDEX unless 0 <= cu[0] <= cu[1] <= ... <= cu[S] <= N.
-__device__ __forceinline__ void check_layout(const SeqLayout& q, uint32_t* status) {
-  if (!q.cu) return;
+// Records KD_ERR_BAD_INDEX unless 0 <= cu[0] <= cu[1] <= ... <= cu[S] <= N; true where this
+// thread has seen that it is not so.  The loss of such a batch is NaN, for callers that
+// do not read the status.
+__device__ __forceinline__ bool check_layout(const SeqLayout& q, uint32_t* status) {
+  bool bad = false;
+  if (!q.cu) return false;
   for (int64_t b = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; b <= q.S;
        b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int32_t x = __ldg(q.cu + b);
     const int32_t y = b < q.S ? __ldg(q.cu + b + 1) : q.N;
-    if (x < 0 || x > y || x > q.N) set_status(status, KD_ERR_BAD_INDEX);
+    if (x < 0 || x > y || x > q.N) bad = true;
   }
+  if (bad) set_status(status, KD_ERR_BAD_INDEX);
+  return bad;
+}
+// The same for a block that checks by itself, in every thread (a barrier).
+__device__ __forceinline__ bool check_layout_block(const SeqLayout& q, uint32_t* status) {
+  return q.cu && __syncthreads_or(check_layout(q, status));
+}
+// What the blocks of this grid, all of which have checked, or of an earlier one have seen.
+__device__ __forceinline__ bool layout_bad(const SeqLayout& q, const uint32_t* status) {
+  return q.cu && __ldcg(status) != 0u;
+}
+__device__ __forceinline__ float loss_out(double loss, bool bad) {
+  return bad ? __int_as_float(0x7FC00000) : static_cast<float>(loss);
 }
 
 // ----------------------------------------------------------------------------
@@ -609,9 +625,10 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
   v[3] = n_clip;
 }
 
-__device__ __forceinline__ void policy_write(const PolicyArgs& a, const double (&v)[POLICY_STATS]) {
+__device__ __forceinline__ void policy_write(const PolicyArgs& a, const double (&v)[POLICY_STATS],
+                                             bool bad) {
   const double n = v[1] > 0.0 ? v[1] : 1.0;
-  *a.loss = static_cast<float>(v[0]);
+  *a.loss = loss_out(v[0], bad);
   a.stats[0] = static_cast<float>(v[1]);
   a.stats[1] = static_cast<float>(v[2] / n);
   a.stats[2] = static_cast<float>(v[3] / n);
@@ -679,13 +696,14 @@ policy_main_kernel(const PolicyArgs a) {
 #pragma unroll
     for (int i = 0; i < POLICY_STATS; ++i) a.partials[blockIdx.x * POLICY_STATS + i] = v[i];
   if (!last_block(a.ticket, &flag)) return;
+  const bool bad = layout_bad(a.seq, a.status);
 #pragma unroll
   for (int i = 0; i < POLICY_STATS; ++i) v[i] = 0.0;
   for (uint32_t k = threadIdx.x; k < gridDim.x; k += blockDim.x)
 #pragma unroll
     for (int i = 0; i < POLICY_STATS; ++i) v[i] += __ldcg(a.partials + k * POLICY_STATS + i);
   block_sum(v, sm);
-  if (threadIdx.x == 0) policy_write(a, v);
+  if (threadIdx.x == 0) policy_write(a, v, bad);
 }
 
 // The whole loss in one block, for batches where launches cost more than the
@@ -710,11 +728,11 @@ __global__ void __launch_bounds__(OBJ_THREADS, 1) policy_one_kernel(const Policy
     n_all = block_count(policy_count_all(a, threadIdx.x, OBJ_THREADS), counts);
   }
   __syncthreads();
-  check_layout(a.seq, a.status);
+  const bool bad = check_layout_block(a.seq, a.status);
   double v[POLICY_STATS] = {};
   policy_tokens<OLD, REF>(a, queue, warp, NW, n_all, ahead, lane, v);
   block_sum(v, sm);
-  if (threadIdx.x == 0) policy_write(a, v);
+  if (threadIdx.x == 0) policy_write(a, v, bad);
 }
 
 // ----------------------------------------------------------------------------
@@ -1042,10 +1060,11 @@ __global__ void __launch_bounds__(OBJ_THREADS) pref_tokens_kernel(const PrefArgs
   griddep_wait();                            // the pairs
   if (a.dlogp) pref_tokens(a, row, (gridDim.x * OBJ_THREADS) >> 5, m, lane);
   if (blockIdx.x != gridDim.x - 1) return;
+  const bool bad = layout_bad(a.seq, a.status);
   double v[1] = {0.0};
   for (int k = threadIdx.x; k < n_partials; k += OBJ_THREADS) v[0] += __ldcg(a.partials + k);
   block_sum(v, sm);
-  if (threadIdx.x == 0) *a.loss = static_cast<float>(v[0] * a.inv_pairs);
+  if (threadIdx.x == 0) *a.loss = loss_out(v[0] * a.inv_pairs, bad);
 }
 
 // The three steps in one block, for batches where launches cost more than the
@@ -1060,10 +1079,10 @@ __global__ void __launch_bounds__(OBJ_THREADS, 1) pref_one_kernel(const PrefArgs
   for (int32_t i = warp; i < a.n_spans; i += NW)
     pref_sums<SHORT>(a, rows + warp * PREF_SMEM, i, lane);
   __syncthreads();
-  check_layout(a.seq, a.status);
+  const bool bad = check_layout_block(a.seq, a.status);
   double v[1] = {pref_pairs(a, warp, NW, lane)};
   block_sum(v, sm);                          // its barriers also publish the gradients
-  if (threadIdx.x == 0) *a.loss = static_cast<float>(v[0] * a.inv_pairs);
+  if (threadIdx.x == 0) *a.loss = loss_out(v[0] * a.inv_pairs, bad);
   if (a.dlogp)
     pref_tokens(a, warp, NW, load_mask4(a.mask, 4 * threadIdx.x, a.seq.N, a.mask_vec), lane);
 }

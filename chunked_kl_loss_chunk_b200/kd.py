@@ -757,7 +757,9 @@ def policy_loss(logp, old_logp, advantages, *, mask=None, ref_logp=None, cu_seql
     [sequences], or like ``logp`` with ``advantages_per="token"``.
     ``reduction``: "token", "sequence" or "fixed" (with ``denom``).  ``stats``:
     tokens that count, and over them the means of the ratio, of "clipped" and
-    of the KL estimate.  ``dlogp`` is what ``head_logprobs_bwd`` takes."""
+    of the KL estimate.  ``dlogp`` is what ``head_logprobs_bwd`` takes.  A
+    ``cu_seqlens`` that does not ascend within the tokens makes the loss NaN (and
+    KD_ERR_BAD_INDEX in a given ``ws``)."""
     lib = load()
     if stream is None and reduction in REDUCTIONS and advantages_per in ADVANTAGES_PER and \
             (reduction == "fixed") == (denom is not None):
@@ -826,7 +828,8 @@ def preference_loss(logp, *, ref_logp=None, mask=None, cu_seqlens=None, kind: st
     [2 pairs + 1]: first every pair's chosen sequence, then every pair's rejected
     one.  ``ref_logp`` (None: no reference) and ``mask`` like ``logp``.  ``kind``:
     "sigmoid" (with ``label_smoothing``), "hinge" or "ipo".  ``pairs_total``: the
-    pairs of the whole batch when these are a part of it."""
+    pairs of the whole batch when these are a part of it.  A bad ``cu_seqlens``
+    as for ``policy_loss``."""
     lib = load()
     if stream is None and kind in PREFERENCE_KINDS:
         out = _native.preference_loss(logp, ref_logp, mask, cu_seqlens, PREFERENCE_KINDS[kind], beta, margin,

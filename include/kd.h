@@ -317,8 +317,8 @@ kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T
 /*   cu_seqlens int32 [n_seqs + 1] (device), 0 <= cu[0] <= ... <= cu[n_seqs]  */
 /*     <= n_tokens: sequence b is the tokens [cu[b], cu[b + 1]), and may be  */
 /*     empty; or NULL: rows of n_tokens / n_seqs tokens (no remainder).      */
-/*     Any other cu is recorded as KD_ERR_BAD_INDEX, with unspecified (but   */
-/*     in-bounds) outputs.                                                   */
+/*     Any other cu is recorded as KD_ERR_BAD_INDEX, and the loss is NaN; the */
+/*     other outputs are then unspecified (all accesses stay in bounds).     */
 /*   mask [n_tokens], one byte a token, 0: the token does not count; NULL:   */
 /*     every token counts.  What the other arrays hold at a token that does  */
 /*     not count, or that lies outside every sequence, is never used (it may */

@@ -31,3 +31,39 @@ def test_a_bad_target_in_the_autograd_form():
     tgt[3] = -1                                        # a padding label of another program
     out = kd.HeadLogprobs.apply(h.requires_grad_(), W, tgt, 40)
     assert bool(torch.isnan(out[3])) and not bool(torch.isnan(out[tgt != -1]).any())
+
+
+BAD_CU = {
+    "negative": lambda cu, n: cu.__setitem__(0, -1),
+    "past the tokens": lambda cu, n: cu.__setitem__(-1, n + 1),
+    "far past them": lambda cu, n: cu.__setitem__(3, 2 ** 31 - 1),
+    "descending": lambda cu, n: cu.__setitem__(2, cu[3].item() + 1),
+    "last": lambda cu, n: cu.__setitem__(-1, cu[-2].item() - 1),
+}
+
+
+@pytest.mark.parametrize("length", [7, 900])          # in one block, and in several
+@pytest.mark.parametrize("bad", BAD_CU)
+def test_a_bad_layout_makes_the_loss_nan(length, bad):
+    require_gpu()
+    S = 8
+    n = S * length + 5
+    cu = (torch.arange(S + 1, dtype=torch.int32) * length + 2).cuda()
+    logp = torch.full((n,), -1.0, device="cuda")
+    adv = torch.ones(S, device="cuda")
+    wrong = cu.clone()
+    BAD_CU[bad](wrong, n)
+    for mask in (None, torch.ones(n, dtype=torch.bool, device="cuda")):
+        for reduction in ("token", "sequence"):
+            for grad in (True, False):
+                kw = dict(mask=mask, reduction=reduction, grad=grad)
+                assert kd.policy_loss(logp, logp, adv, cu_seqlens=cu, **kw)[0].item() == -1.0
+                assert torch.isnan(kd.policy_loss(logp, logp, adv, cu_seqlens=wrong, **kw)[0])
+        for grad in (True, False):
+            good = kd.preference_loss(logp, mask=mask, cu_seqlens=cu, grad=grad)[0]
+            assert good.item() == pytest.approx(0.6931472, rel=1e-6)
+            assert torch.isnan(kd.preference_loss(logp, mask=mask, cu_seqlens=wrong, grad=grad)[0])
+    # a call without a bad layout on the same workspace is a call as ever
+    ws = kd.alloc_workspace(kd.kd_policy_loss_workspace_size(S, n), "cuda")
+    assert torch.isnan(kd.policy_loss(logp, logp, adv, cu_seqlens=wrong, ws=ws)[0])
+    assert kd.policy_loss(logp, logp, adv, cu_seqlens=cu, ws=ws)[0].item() == -1.0
