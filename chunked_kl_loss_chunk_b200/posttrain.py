@@ -26,10 +26,12 @@ class Step(NamedTuple):
     logp: torch.Tensor        # f32, like targets
     dH: torch.Tensor          # [T, d], dtype of h
     dW: torch.Tensor          # [V, d] f32
-    ws: torch.Tensor          # the head's workspace, for kd.read_device_status or the next step
+    ws: torch.Tensor          # the head's workspace, for the next step, with the step's errors in device data
+                              # (a bad target or cu_seqlens) for kd.read_device_status
 
 
-def _through_head(h, W, targets, objective, options, chunk, temperature, ws, dW, accumulate_dW):
+def _through_head(h, W, targets, objective, objective_bytes, cu_seqlens, options, chunk, temperature, ws, dW,
+                  accumulate_dW):
     for name in ("grad", "stream"):        # the step needs the gradient, and all of it on one stream
         if name in options:
             raise TypeError(f"{name}: not an option of a step")
@@ -42,9 +44,16 @@ def _through_head(h, W, targets, objective, options, chunk, temperature, ws, dW,
                                                                kd.KD_HEAD_KEEP)
     logp, lse, ws = kd.head_logprobs(h, W, flat, chunk, temperature, ws=ws, backward=True, keep=keep)
     shaped = logp.view(targets.shape)
-    loss, extra, dlogp = objective(shaped, targets != kd.KD_TARGET_IGNORE)
+    # only packed sequences can be wrong in the objective's device data
+    own = None
+    if cu_seqlens is not None:
+        own = kd.alloc_workspace(objective_bytes(max(cu_seqlens.numel() - 1, 1), flat.numel()), h.device)
+    loss, extra, dlogp = objective(shaped, targets != kd.KD_TARGET_IGNORE, own)
     dH, dW, _ = kd.head_logprobs_bwd(h, W, flat, lse, dlogp.view(-1), chunk, temperature, ws=ws, dW=dW,
                                      accumulate_dW=accumulate_dW, kept_logp=logp if keep else None)
+    if own is not None:                # each pass through the head clears its status: joined at the end
+        status, more = (x[:4].view(torch.int32) for x in (ws, own))
+        torch.maximum(status, more, out=status)
     return Step(loss, extra, shaped, dH, dW, ws)
 
 
@@ -59,9 +68,9 @@ def policy_step(h, W, targets, old_logp, advantages, *, chunk: int, temperature:
     ``kd.policy_loss`` (clip_low, clip_high, kl_coef, reduction, denom,
     advantages_per).  For micro-batches, ``reduction="fixed"`` with the batch's
     token count and ``accumulate_dW=True`` add up to the batch's gradient."""
-    return _through_head(h, W, targets, lambda logp, mask: kd.policy_loss(
-        logp, old_logp, advantages, mask=mask, ref_logp=ref_logp, cu_seqlens=cu_seqlens, **options),
-        options, chunk, temperature, ws, dW, accumulate_dW)
+    return _through_head(h, W, targets, lambda logp, mask, own: kd.policy_loss(
+        logp, old_logp, advantages, mask=mask, ref_logp=ref_logp, cu_seqlens=cu_seqlens, ws=own, **options),
+        kd.kd_policy_loss_workspace_size, cu_seqlens, options, chunk, temperature, ws, dW, accumulate_dW)
 
 
 def preference_step(h, W, targets, *, chunk: int, temperature: float = 1.0, ref_logp=None, cu_seqlens=None,
@@ -71,6 +80,6 @@ def preference_step(h, W, targets, *, chunk: int, temperature: float = 1.0, ref_
     ``targets`` as for ``policy_step``, over 2 pairs sequences: the chosen
     answers, then the rejected ones.  ``options`` go to ``kd.preference_loss``
     (kind, beta, margin, label_smoothing, length_normalize, pairs_total)."""
-    return _through_head(h, W, targets, lambda logp, mask: kd.preference_loss(
-        logp, ref_logp=ref_logp, mask=mask, cu_seqlens=cu_seqlens, **options),
-        options, chunk, temperature, ws, dW, accumulate_dW)
+    return _through_head(h, W, targets, lambda logp, mask, own: kd.preference_loss(
+        logp, ref_logp=ref_logp, mask=mask, cu_seqlens=cu_seqlens, ws=own, **options),
+        lambda n_seqs, n: kd.kd_preference_loss_workspace_size(max(n_seqs // 2, 1), n), cu_seqlens, options, chunk, temperature, ws, dW, accumulate_dW)

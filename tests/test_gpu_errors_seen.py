@@ -4,7 +4,7 @@ the outputs too, for callers that do not read a workspace's status."""
 import pytest
 import torch
 
-from chunked_kl_loss_chunk_b200 import kd
+from chunked_kl_loss_chunk_b200 import kd, posttrain
 from gpu_util import require_gpu
 from test_gpu_head_logprob import _inputs
 
@@ -67,3 +67,33 @@ def test_a_bad_layout_makes_the_loss_nan(length, bad):
     ws = kd.alloc_workspace(kd.kd_policy_loss_workspace_size(S, n), "cuda")
     assert torch.isnan(kd.policy_loss(logp, logp, adv, cu_seqlens=wrong, ws=ws)[0])
     assert kd.policy_loss(logp, logp, adv, cu_seqlens=cu, ws=ws)[0].item() == -1.0
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("kind", ["policy", "preference"])
+def test_a_step_reports_what_its_stages_found(kind, given):
+    require_gpu()
+    T, d, V, chunk, S = 300, 64, 700, 64, 4
+    h, W, tgt, _ = _inputs(T, d, V, torch.bfloat16, seed=8)
+    adv = torch.ones(S, device="cuda")
+    cu = torch.tensor([0, 100, 100, 250, 300], dtype=torch.int32, device="cuda")
+    far = torch.tensor([0, 100, 90, 250, 301], dtype=torch.int32, device="cuda")
+    lost = tgt.clone()
+    lost[5] = V
+    ws = None
+    if given:
+        ws = kd.alloc_workspace(kd.kd_head_logprob_workspace_size(T, d, V, chunk, kd.KD_DTYPE_BF16, kd.KD_HEAD_KEEP),
+                                "cuda")
+
+    def step(targets, layout):
+        if kind == "policy":
+            old = torch.full_like(targets, -6, dtype=torch.float32)
+            return posttrain.policy_step(h, W, targets, old, adv, chunk=chunk, cu_seqlens=layout, ws=ws)
+        return posttrain.preference_step(h, W, targets, chunk=chunk, cu_seqlens=layout, ws=ws)
+
+    for targets, layout in ((tgt, cu), (tgt, far), (lost, cu), (lost, far), (tgt, cu)):
+        out = step(targets, layout)
+        fine = targets is tgt and layout is cu
+        assert kd.read_device_status(out.ws) == (kd.KD_OK if fine else kd.KD_ERR_BAD_INDEX)
+        assert bool(torch.isnan(out.loss)) != fine
+        assert not given or out.ws.data_ptr() == ws.data_ptr()
