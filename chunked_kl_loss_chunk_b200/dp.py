@@ -99,22 +99,26 @@ def clip_grad_norm(replicated, sharded, max_norm: float, *, compute: Callable = 
     """Clips a data-parallel step's gradients in place to the norm over the whole
     batch, and returns that norm (the same on every rank).
 
-    `replicated`: tensors that every rank holds alike (dW after ``shard_step``),
-    counted once; `sharded`: each rank's own rows (dH), whose sums of squares are
-    added over the ranks.  Either may be empty, also on some ranks only: every
-    rank joins the one all-reduce (of a fp64 scalar on `device`, by default the
-    tensors')."""
+    `replicated`: tensors that every rank holds alike (dW after ``shard_step``), counted
+    once whichever ranks hold them, but a rank holds all of them or none; `sharded`: each
+    rank's own part of what is split over the ranks, whose sums of squares are added.
+    Either may be empty, also on some ranks only: every rank joins the one all-reduce
+    (of three fp64 values on `device`, by default the tensors')."""
     replicated = [t for t in replicated if t.numel()]
     sharded = [t for t in sharded if t.numel()]
     both = replicated + sharded
     if device is None:
         device = both[0].device if both else torch.device("cpu")
-    total = compute(sharded, None) if sharded else torch.zeros((), dtype=torch.float64, device=device)
+    zero = torch.zeros((), dtype=torch.float64, device=device)
+    # sums of squares of the two lists, and whether this rank holds the first: the mean over
+    # the ranks that do counts the replicated tensors once, and is the same on every rank
+    parts = torch.stack([compute(sharded, None) if sharded else zero,
+                         compute(replicated, None) if replicated else zero,
+                         zero + float(bool(replicated))])
     world = dist.get_world_size(group) if dist.is_available() and dist.is_initialized() else 1
     if world > 1:
-        dist.all_reduce(total, op=dist.ReduceOp.SUM, group=group)
-    if replicated:
-        total = total + compute(replicated, None)
+        dist.all_reduce(parts, op=dist.ReduceOp.SUM, group=group)
+    total = parts[0] + parts[1] / parts[2].clamp(min=1.0)
     if both:
         return compute(both, max_norm, total)
     return total.sqrt().to(torch.float32)
