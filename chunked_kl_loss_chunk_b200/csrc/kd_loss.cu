@@ -267,11 +267,16 @@ __global__ void __launch_bounds__(1024)
 prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict__ grad, int64_t T,
                    int64_t V, int32_t* __restrict__ idx_sorted, float* __restrict__ p_sorted,
                    float2* __restrict__ stats, uint32_t* status) {
-  griddep_launch_dependents();
   if (gridDim.x == 1) {
-    if (threadIdx.x == 0) *status = 0u;
+    // before the next kernel may start: its waits read the word, and a call's word may hold
+    // anything (an earlier call's timeout, a fresh allocation's bytes)
+    if (threadIdx.x == 0) {
+      *status = 0u;
+      __threadfence();
+    }
     __syncthreads();
   }
+  griddep_launch_dependents();
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < T;
        t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int32_t y = targets[t];
