@@ -516,7 +516,6 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
   const float seqs = static_cast<float>(q.S);
   uint32_t n_tok = 0, n_clip = 0;
   F2 s_loss = f2(0.f), s_ratio = f2(0.f), s_kl = f2(0.f);
-  uint32_t n_seen = 0;
   int held = 0;
   for (int slot = 0; row < n_rows; row += n_warps, slot = slot + 1 == POLICY_DEPTH ? 0 : slot + 1) {
     const int32_t t0 = row * 128 + 4 * lane;
@@ -551,8 +550,9 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
           for (int j = 0; j < 4; ++j) policy_look(a, b[j], seqs, at[j], wt[j]);
         }
       }
-      // What a token that does not count holds is replaced before it is used: with its A, d and
-      // x at 0, every term below is 0 and the ratio 1.
+      // What a token that does not count holds is replaced before it is used: with its A and x at
+      // 0 and its d at -inf, every term below and its ratio are 0 (a ratio of 1, to be taken off
+      // at the end, would cost ratios far below one their digits).
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
         const bool on0 = mask_byte(m, j), on1 = mask_byte(m, j + 1);
@@ -562,8 +562,8 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
         F2 ratio = f2(1.f);
         if (OLD) {
           f2_get(add2(f2(od[j], od[j + 1]), nlp), d0, d1);      // -d
-          d0 = on0 ? -d0 : 0.f;
-          d1 = on1 ? -d1 : 0.f;
+          d0 = on0 ? -d0 : -INFINITY;
+          d1 = on1 ? -d1 : -INFINITY;
           ratio = exp2v(f2(d0, d1));
           s_ratio = add2(s_ratio, ratio);
         }
@@ -605,7 +605,6 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
         f2_get(mul2(nw, grad), out[j], out[j + 1]);
       }
       n_tok += __popc(byte_flags(m));
-      n_seen += 4;
       if (++held == 16) {
         policy_add(v, s_loss, s_ratio, s_kl);
         s_loss = s_ratio = s_kl = f2(0.f);
@@ -620,8 +619,7 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const PolicyQ
   }
   policy_add(v, s_loss, s_ratio, s_kl);
   v[1] = n_tok;
-  if (OLD) v[2] -= n_seen - n_tok;           // the ratios of 1 of tokens that do not count
-  else v[2] = n_tok;
+  if (!OLD) v[2] = n_tok;
   v[3] = n_clip;
 }
 
