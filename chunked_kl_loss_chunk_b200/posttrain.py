@@ -27,7 +27,7 @@ class Step(NamedTuple):
     dH: torch.Tensor          # [T, d], dtype of h
     dW: torch.Tensor          # [V, d] f32
     ws: torch.Tensor          # the head's workspace, for the next step, with the step's errors in device data
-                              # (a bad target or cu_seqlens) for kd.read_device_status
+                              # (a bad target or cu_seqlens) or its waits for kd.read_device_status
 
 
 def _through_head(h, W, targets, objective, objective_bytes, cu_seqlens, options, chunk, temperature, ws, dW,
@@ -43,17 +43,20 @@ def _through_head(h, W, targets, objective, objective_bytes, cu_seqlens, options
         keep = ws.numel() >= kd.kd_head_logprob_workspace_size(*h.shape, W.shape[0], chunk, kd._dtype_code(h),
                                                                kd.KD_HEAD_KEEP)
     logp, lse, ws = kd.head_logprobs(h, W, flat, chunk, temperature, ws=ws, backward=True, keep=keep)
+    status = ws[:4].view(torch.int32)
+    found = [status.clone()]           # the backward clears the forward's
     shaped = logp.view(targets.shape)
     # only packed sequences can be wrong in the objective's device data
     own = None
     if cu_seqlens is not None:
         own = kd.alloc_workspace(objective_bytes(max(cu_seqlens.numel() - 1, 1), flat.numel()), h.device)
     loss, extra, dlogp = objective(shaped, targets != kd.KD_TARGET_IGNORE, own)
+    if own is not None:
+        found.append(own[:4].view(torch.int32))
     dH, dW, _ = kd.head_logprobs_bwd(h, W, flat, lse, dlogp.view(-1), chunk, temperature, ws=ws, dW=dW,
                                      accumulate_dW=accumulate_dW, kept_logp=logp if keep else None)
-    if own is not None:                # each pass through the head clears its status: joined at the end
-        status, more = (x[:4].view(torch.int32) for x in (ws, own))
-        torch.maximum(status, more, out=status)
+    for code in found:                 # of several errors the one that stopped more work
+        torch.maximum(status, code, out=status)
     return Step(loss, extra, shaped, dH, dW, ws)
 
 
