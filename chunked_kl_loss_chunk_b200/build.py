@@ -3,6 +3,8 @@
 Usage: ``python -m chunked_kl_loss_chunk_b200.build`` (or ``build()``).
 The library is written next to this file so it travels with the repository, and
 beside it _kd_native.so, the C++ half of the Python binding (torch's headers, g++).
+``--lib-only`` (``build(native=False)``) leaves that out, for programs in C: kd.py
+then makes every call through ctypes.
 """
 
 from __future__ import annotations
@@ -24,6 +26,8 @@ LIB_PATH = os.path.join(PKG_DIR, "libkd.so")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libkd_debug.so")
 NATIVE_SRC = os.path.join(CSRC, "kd_native.cpp")
 NATIVE_PATH = os.path.join(PKG_DIR, "_kd_native.so")
+# what the module was last built for: its file's time does not tell an upgrade of torch or Python
+NATIVE_STAMP = os.path.join(ROOT, "_build", "_kd_native.built_for")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -57,10 +61,26 @@ def up_to_date(debug: bool = False) -> bool:
     return all(os.path.getmtime(p) <= t for p in deps())
 
 
+def _built_for() -> str:
+    """The Python and torch whose ABI the module is compiled against."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return f"python {'.'.join(map(str, sys.version_info[:3]))}, torch {torch.__version__}, cxx11 abi {abi}\n"
+
+
+def native_up_to_date() -> bool:
+    newest = max(os.path.getmtime(p) for p in (NATIVE_SRC, os.path.join(INCLUDE, "kd.h")))
+    if not os.path.exists(NATIVE_PATH) or os.path.getmtime(NATIVE_PATH) < newest:
+        return False
+    if not os.path.exists(NATIVE_STAMP):
+        return False
+    with open(NATIVE_STAMP) as f:
+        return f.read() == _built_for()
+
+
 def build_native(force: bool = False, verbose: bool = False) -> str:
     """Compile _kd_native.so against the installed torch; returns its path."""
-    newest = max(os.path.getmtime(p) for p in (NATIVE_SRC, os.path.join(INCLUDE, "kd.h")))
-    if not force and os.path.exists(NATIVE_PATH) and os.path.getmtime(NATIVE_PATH) >= newest:
+    if not force and native_up_to_date():
         return NATIVE_PATH
     import torch
     home = os.path.dirname(torch.__file__)
@@ -76,14 +96,24 @@ def build_native(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, NATIVE_PATH)
+    os.makedirs(os.path.dirname(NATIVE_STAMP), exist_ok=True)
+    with open(NATIVE_STAMP, "w") as f:
+        f.write(_built_for())
     return NATIVE_PATH
 
 
-def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
+def build(force: bool = False, verbose: bool = False, debug: bool = False, native: bool = True) -> str:
     """Compile every CUDA source into one shared library; returns its path.
-    ``debug`` builds libkd_debug.so, with the device-side invariant checks."""
+    ``debug`` builds libkd_debug.so, with the device-side invariant checks;
+    ``native=False`` leaves out the C++ half of the Python binding."""
+    lib = _build_lib(force, verbose, debug)
+    if native:
+        build_native(force and not debug, verbose)
+    return lib
+
+
+def _build_lib(force: bool, verbose: bool, debug: bool) -> str:
     lib = DEBUG_LIB_PATH if debug else LIB_PATH
-    build_native(force and not debug, verbose)
     if not force and up_to_date(debug):
         return lib
     nvcc = _nvcc()
@@ -107,4 +137,5 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose=True, debug="--debug" in sys.argv))
+    print(build(force="--force" in sys.argv, verbose=True, debug="--debug" in sys.argv,
+                native="--lib-only" not in sys.argv))

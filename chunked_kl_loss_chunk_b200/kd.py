@@ -23,6 +23,7 @@ import ctypes
 import operator
 import os
 import re
+import warnings
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -118,7 +119,11 @@ def header_symbols():
 
 
 def load():
-    """Load libkd.so (raises if it is missing: there is no fallback)."""
+    """Load libkd.so (raises if it is missing: there is no fallback), and
+    _kd_native.so, the short way to the post-training calls.  Where that one is
+    not to be had (only the library was built, or for another torch), a warning
+    says so once and those calls are made through ctypes: the same kernels, and
+    some 10 us more of host time a call."""
     global _lib, _native
     if _lib is not None:
         return _lib
@@ -132,10 +137,13 @@ def load():
     try:
         from chunked_kl_loss_chunk_b200 import _kd_native
     except ImportError as e:
-        raise RuntimeError(f"_kd_native.so not built or not loadable ({e}); "
-                           "run chunked_kl_loss_chunk_b200.build") from e
-    _kd_native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS))
-    _lib, _native = lib, _kd_native
+        warnings.warn(f"_kd_native.so not built or not loadable ({e}): post-training calls go through ctypes; "
+                      "run chunked_kl_loss_chunk_b200.build", RuntimeWarning, stacklevel=2)
+        _native = None
+    else:
+        _kd_native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS))
+        _native = _kd_native
+    _lib = lib
     return lib
 
 
@@ -596,7 +604,7 @@ def head_logprobs(h, W, targets, chunk: int, temperature: float = 1.0, ws=None, 
     ``kept_logp=logp``, and let nothing else use ``ws`` in between."""
     use = KD_HEAD_KEEP if keep else (KD_HEAD_BOTH if backward else KD_HEAD_FWD)
     load()
-    if stream is None:
+    if stream is None and _native is not None:
         out = _native.head_logprobs(h, W, targets, chunk, temperature, use, ws)
         if out is not None:
             return _native_result(out, "kd_head_logprob_fwd")
@@ -629,7 +637,7 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
     place).  ``kept_logp`` and ``ws`` of a forward with ``keep=True``: its
     exponentials take the place of recomputed logits, and are used up."""
     load()
-    if stream is None and dH is None and dW is None and not accumulate_dW and any(need) and \
+    if stream is None and _native is not None and dH is None and dW is None and not accumulate_dW and any(need) and \
             (dW_dtype is torch.float32 or dW_dtype is torch.bfloat16):
         out = _native.head_logprobs_bwd(h, W, targets, lse, kept_logp, grad_logp, grad_loss, chunk, temperature,
                                         need[0], need[1], dW_dtype is torch.bfloat16, ws)
@@ -761,7 +769,7 @@ def policy_loss(logp, old_logp, advantages, *, mask=None, ref_logp=None, cu_seql
     ``cu_seqlens`` that does not ascend within the tokens makes the loss NaN (and
     KD_ERR_BAD_INDEX in a given ``ws``)."""
     lib = load()
-    if stream is None and reduction in REDUCTIONS and advantages_per in ADVANTAGES_PER and \
+    if stream is None and _native is not None and reduction in REDUCTIONS and advantages_per in ADVANTAGES_PER and \
             (reduction == "fixed") == (denom is not None):
         out = _native.policy_loss(logp, old_logp, ref_logp, advantages, advantages_per == "token", mask,
                                   cu_seqlens, clip_low, clip_high, kl_coef, REDUCTIONS[reduction],
@@ -831,7 +839,7 @@ def preference_loss(logp, *, ref_logp=None, mask=None, cu_seqlens=None, kind: st
     pairs of the whole batch when these are a part of it.  A bad ``cu_seqlens``
     as for ``policy_loss``."""
     lib = load()
-    if stream is None and kind in PREFERENCE_KINDS:
+    if stream is None and _native is not None and kind in PREFERENCE_KINDS:
         out = _native.preference_loss(logp, ref_logp, mask, cu_seqlens, PREFERENCE_KINDS[kind], beta, margin,
                                       label_smoothing, length_normalize, pairs_total, grad, ws)
         if out is not None:
@@ -929,7 +937,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, sumsq=None, stream=None):
     a part of what the norm is taken over (``dp.clip_grad_norm``)."""
     lib = load()
     grads, out = list(grads), None if out is None else list(out)
-    if stream is None:
+    if stream is None and _native is not None:
         done = _native.clip_grad_norm(grads, out, max_norm, sumsq)
         if done is not None:
             return _native_result(done, "kd_grad_clip")[0]
