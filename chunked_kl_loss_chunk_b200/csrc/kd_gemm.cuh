@@ -241,8 +241,11 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
       const float gl = g.grad_loss ? __ldg(g.grad_loss) : 1.f;
       const float coef = gl * g.inv_T_tau;
       float coefA = 0.f, off = 0.f;
+      bool none = false;               // a row without a term: 0, whatever its logits are
       if (row_ok) {
-        coefA = coef * g.row_stats[t].x;
+        const float S = g.row_stats[t].x;
+        none = S == 0.f;
+        coefA = coef * S;
         off = -__ldg(g.lse + t) * 1.4426950408889634f;   // -LSE * log2(e)
       }
 #pragma unroll 1
@@ -253,8 +256,13 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& g, const CUtensorMa
         box_reuse_wait();
         float v[32];
         tmem_ld32(taddr + c * 32, v);
+        if (none) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = coefA * ex2_approx(fmaf(v[j], zs, off));
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = coefA * ex2_approx(fmaf(v[j], zs, off));
+        }
         if (nidx < base + 32) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {

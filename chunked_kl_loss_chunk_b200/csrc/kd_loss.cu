@@ -400,7 +400,9 @@ kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float z
       const int64_t t = row0 + r;
       if (t >= T || col >= V) continue;
       const float k = scale[r][lane * VEC / 32];
-      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+      // a row without a target may have kept anything: 0 in its place
+      const uint32_t some = ys[r] != INT32_MAX ? 0xFFFFFFFFu : 0u;
+      const uint32_t w[4] = {q[i].x & some, q[i].y & some, q[i].z & some, q[i].w & some};
       float x[VEC];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -429,6 +431,24 @@ kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float z
       *reinterpret_cast<uint4*>(dz + t * ldz + col) = out;
     }
     __syncthreads();
+  }
+}
+
+// h for dW = dz^T h, with zeros in the rows that have no target: what a trunk left
+// there (NaN of attention over nothing, infinities) times their dz of 0 would be NaN.
+// Elementwise, 16 bytes a thread; the dW GEMM then reads `out` in the place of h.  The
+// copy is made whether or not a row is ignored, which only the device knows: 4 bytes an
+// element beside 6 V flops of each.
+__global__ void __launch_bounds__(256)
+target_rows_kernel(const uint4* __restrict__ h, const int32_t* __restrict__ target, int64_t rows,
+                   int64_t per_row, uint4* __restrict__ out) {
+  griddep_launch_dependents();
+  griddep_wait();                       // the prepared rows, and what `out` held before
+  const int64_t n = rows * per_row;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const bool none = target[i / per_row] == INT32_MAX;
+    out[i] = none ? make_uint4(0u, 0u, 0u, 0u) : h[i];
   }
 }
 
@@ -980,6 +1000,19 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
     // (3) dW (+)= dz_g^T h_g over the group: M = V, N = d, K = grows; both
     //     operands MN-major
     const Elem* hg = static_cast<const Elem*>(h) + g0 * d;
+    if (rt.targets) {
+      // into the place of the dH partials, which the group has done with: at most
+      // KD_DW_GROUP rows_pad d operands in KD_DH_MAX_SPLIT rows_pad d floats
+      static_assert(KD_DW_GROUP * sizeof(Elem) <= KD_DH_MAX_SPLIT * sizeof(float), "h fits");
+      const int64_t per_row = d * sizeof(Elem) / 16;
+      int64_t blocks = (grows * per_row + 255) / 256;
+      if (blocks > 8 * static_cast<int64_t>(num_sms)) blocks = 8 * static_cast<int64_t>(num_sms);
+      if (launch_pdl(target_rows_kernel, dim3(static_cast<unsigned>(blocks)), 256u, s,
+                     reinterpret_cast<const uint4*>(hg), static_cast<const int32_t*>(idx_s + g0),
+                     grows, per_row, reinterpret_cast<uint4*>(hpart)) != cudaSuccess)
+        return KD_ERR_CUDA;
+      hg = reinterpret_cast<const Elem*>(hpart);
+    }
     CUtensorMap tH_mn, tDz_mn;
     if (!make_map(&tH_mn, hg, F32, d, grows, d, INNER, BK, true)) return KD_ERR_CUDA;
     if (!make_map(&tDz_mn, dz, F32, V, grows, L.ldz, INNER, BK, true)) return KD_ERR_CUDA;

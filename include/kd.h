@@ -299,8 +299,9 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
  * once more (each dz entry but the target's has two roundings in place of one).
  * A row with a bad target (recorded as KD_ERR_BAD_INDEX) adds nothing to either.
  * Either of dH and dW may be NULL: that gradient is not computed (a frozen head
- * needs no dW).  dz is rounded to the operands' type, as in kd_fused_kl_bwd.  An ignored row
- * contributes 0 times its h to dW, so h must be finite in every row.
+ * needs no dW).  dz is rounded to the operands' type, as in kd_fused_kl_bwd.  What h
+ * holds in a row without a token (ignored, or with a bad target) is not used: it may be NaN
+ * or infinite.
  */
 kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                               int64_t V, const int32_t* targets, int64_t chunk, float temperature,
