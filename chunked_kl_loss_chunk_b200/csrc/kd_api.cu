@@ -2,6 +2,7 @@
 // workspace sizing, device status, and dispatch to the kernels.
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <atomic>
 
@@ -130,7 +131,7 @@ kd_status kd_topk_build(const void* logits, int dtype, int64_t T, int64_t V, int
   const int sms = num_sms_current();
   if (sms <= 0) return KD_ERR_CUDA;
   // status word and row counter, both zero before the build
-  if (cudaMemsetAsync(ws, 0, kd::KD_TOPK_COUNTER_OFFSET + 8, s) != cudaSuccess) return KD_ERR_CUDA;
+  if (cudaMemsetAsync(ws, 0, kd::WS_HEADER_BYTES, s) != cudaSuccess) return KD_ERR_CUDA;
   unsigned long long* row_counter = reinterpret_cast<unsigned long long*>(
       static_cast<char*>(ws) + kd::KD_TOPK_COUNTER_OFFSET);
   if (kd::launch_topk_bf16(logits, T, V, K, out_vals, out_idx, static_cast<uint32_t*>(ws),
@@ -297,6 +298,22 @@ size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t c
   return L.total > F.fwd_end ? L.total : F.fwd_end;
 }
 
+// Label of what a forward keeps for a backward of the same sizes, temperature and type, and
+// of chunks that place it alike: FNV-1a (Fowler, Noll and Vo) over these numbers, never 0.
+static uint64_t keep_label(int dtype, int64_t T, int64_t d, int64_t V, int64_t chunk, float tau) {
+  uint32_t tau_bits;
+  memcpy(&tau_bits, &tau, 4);
+  const int64_t bwd = head_bwd_chunk(chunk), fwd = head_fwd_chunk(chunk);
+  const uint64_t of[] = {static_cast<uint64_t>(dtype), static_cast<uint64_t>(T),
+                         static_cast<uint64_t>(d),     static_cast<uint64_t>(V),
+                         static_cast<uint64_t>(bwd < T ? bwd : T),
+                         static_cast<uint64_t>(fwd < T ? fwd : T), tau_bits};
+  uint64_t x = 14695981039346656037ull;
+  for (uint64_t v : of)
+    for (int i = 0; i < 8; ++i, v >>= 8) x = (x ^ (v & 0xFF)) * 1099511628211ull;
+  return x ? x : 1;
+}
+
 // Checks shared by the two calls below.
 static kd_status validate_head(const void* h, const void* W, int dtype, int64_t T, int64_t d,
                                int64_t V, const int32_t* targets, int64_t chunk, float tau,
@@ -332,6 +349,7 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
   kd::RowTerms rt;
   rt.targets = targets;
   rt.keep_chunk = keep ? head_bwd_chunk(chunk) : 0;
+  rt.keep_label = keep ? keep_label(dtype, T, d, V, chunk, temperature) : 0;
   return kd::fused_fwd(h, W, dtype, T, 1, d, V, rt, head_fwd_chunk(chunk), temperature, nullptr,
                        lse, logp, ws, static_cast<cudaStream_t>(stream), sms, kd::wait_limit_ns());
 }
@@ -359,6 +377,7 @@ kd_status kd_head_logprob_bwd(const void* h, const void* W, int dtype, int64_t T
   rt.grad_rows = grad_logp;
   rt.kept_logp = kept_logp;
   rt.keep_chunk = kept_logp ? head_fwd_chunk(chunk) : 0;
+  rt.keep_label = kept_logp ? keep_label(dtype, T, d, V, chunk, temperature) : 0;
   return kd::fused_bwd(h, W, dtype, T, 1, d, V, rt, head_bwd_chunk(chunk), temperature, lse, grad_loss, dH, dW,
                        dW ? dW_dtype : KD_DTYPE_F32, accumulate_dW, ws, static_cast<cudaStream_t>(stream), sms,
                        kd::wait_limit_ns());

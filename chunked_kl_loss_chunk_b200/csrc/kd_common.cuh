@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "kd.h"
+#include "kd_internal.h"
 
 namespace kd {
 
@@ -21,6 +22,20 @@ __device__ __forceinline__ void set_status(uint32_t* status, uint32_t code) {
 
 __device__ __forceinline__ uint32_t read_status(const uint32_t* status) {
   return *reinterpret_cast<const volatile uint32_t*>(status);
+}
+
+// Whether the other threads of a call are to give up: a wait ran out, or an invariant is
+// broken.  (A bad index is an error of its row alone, a workspace without what it should
+// hold one of the results; the work goes on to the end.)
+__device__ __forceinline__ bool stops(uint32_t code) {
+  return code == KD_ERR_TIMEOUT || code == KD_ERR_INTERNAL;
+}
+
+// A call's status word before it starts, and the label of what a head's forward kept in
+// the workspace, which this call is about to use (WS_LABEL_WORD words on).
+__device__ __forceinline__ void clear_status(uint32_t* status) {
+  *status = 0u;
+  *reinterpret_cast<uint64_t*>(status + WS_LABEL_WORD) = 0u;
 }
 
 // Invariant checks of the debug build (compiled with -DKD_DEBUG=1, shipped as
@@ -95,17 +110,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
   return ok != 0;
 }
 
-// A wait that ran out, in the place of a bad index that may be recorded already:
-// the other waits have to see it.
+// A wait that ran out, in the place of an error that does not stop the others and may be
+// recorded already: they have to see it.
 __device__ __forceinline__ void set_timeout(uint32_t* status) {
-  if (atomicCAS(status, 0u, KD_ERR_TIMEOUT) == KD_ERR_BAD_INDEX)
-    atomicCAS(status, static_cast<uint32_t>(KD_ERR_BAD_INDEX), static_cast<uint32_t>(KD_ERR_TIMEOUT));
+  const uint32_t had = atomicCAS(status, 0u, KD_ERR_TIMEOUT);
+  if (had != 0u && !stops(had)) atomicCAS(status, had, static_cast<uint32_t>(KD_ERR_TIMEOUT));
 }
 
 // Wait until the phase with the given parity has completed.  Gives up after
 // `limit_ns` of wall time, recording KD_ERR_TIMEOUT, or as soon as another thread
-// of the call has recorded that or a broken invariant.  (A bad index is an error of
-// its row alone; the other rows are worked on to the end.)  Returns true on success.
+// of the call has recorded an error that stops it.  Returns true on success.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                           uint32_t* status) {
   const uint32_t a = smem_u32(bar);
@@ -114,8 +128,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(a, parity)) return true;
     if ((it & 63u) == 0u) {
-      const uint32_t code = read_status(status);
-      if (code != 0u && code != KD_ERR_BAD_INDEX) return false;
+      if (stops(read_status(status))) return false;
       if (globaltimer_ns() - t0 > limit_ns) {
         set_timeout(status);
         return false;

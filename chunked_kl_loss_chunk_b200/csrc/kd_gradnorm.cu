@@ -134,7 +134,7 @@ grad_sumsq_kernel(const __grid_constant__ GradTable<N> t, double* __restrict__ p
                   uint32_t* status) {
   __shared__ double sm[GRAD_THREADS / 32];
   griddep_launch_dependents();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;      // nothing here can fail later
+  if (blockIdx.x == 0 && threadIdx.x == 0) clear_status(status);      // nothing here can fail later
   double v[1] = {0.0};
   uint4 r[GRAD_VECS];
   for (uint32_t u = blockIdx.x; u < t.units; u += gridDim.x) {
@@ -191,7 +191,7 @@ grad_scale_kernel(const __grid_constant__ GradTable<N> t, const double* __restri
     factor = c >= 1.0 ? 1.f : static_cast<float>(c);          // NaN stays NaN
     if (norm && blockIdx.x == 0) {
       *norm = static_cast<float>(x);
-      *status = 0u;
+      clear_status(status);
     }
   }
   __syncthreads();

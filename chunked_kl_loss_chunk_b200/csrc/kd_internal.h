@@ -9,6 +9,11 @@
 
 namespace kd {
 
+// Header of every workspace, in 32-bit words: the status at 0, a counter or ticket at 2,
+// the label of what a keeping forward of the head left (64 bits) and whether the backward
+// found the label that it needs.
+constexpr int WS_LABEL_WORD = 4, WS_FOUND_WORD = 6, WS_HEADER_BYTES = 32;
+
 // Largest number of K-splits used for dH = dz W (its fp32 partials live in
 // the workspace).
 constexpr int KD_DH_MAX_SPLIT = 4;
@@ -75,6 +80,8 @@ struct RowTerms {
   // is given (keep_chunk is then the forward's chunk).
   int64_t keep_chunk = 0;
   const float* kept_logp = nullptr;
+  // Of what the forward keeps: written by it, looked for by the backward (0 for neither).
+  uint64_t keep_label = 0;
 };
 
 // The fused loss over T positions whose loss and gradients are normalised by
@@ -102,8 +109,7 @@ constexpr int64_t KD_HEAD_FWD_ROWS = 2048;
 // fewer would leave partly empty.
 constexpr int64_t KD_HEAD_BWD_ROWS = 256;
 
-// The top-K build's workspace: the status word at byte 0 and the row counter
-// (zero before each build) at byte 8.
+// The top-K build's row counter (zero before each build) in the workspace's header.
 constexpr size_t KD_TOPK_COUNTER_OFFSET = 8;
 cudaError_t launch_topk_bf16(const void* logits, int64_t T, int64_t V, int K, float* out_vals,
                              int32_t* out_idx, uint32_t* status, unsigned long long* row_counter,

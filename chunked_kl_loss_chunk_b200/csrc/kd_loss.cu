@@ -262,20 +262,29 @@ prep_reg_kernel(const float* __restrict__ vals, const int32_t* __restrict__ idx,
 // log-probability of a row without an entry: 0, or NaN for a bad target, so that it
 // does not go unnoticed where nobody reads the status.  A single block also clears
 // the status word, in the place of a memset before it (2 us of a short call).
+//
+// The label of kept exponentials: a forward writes its own, or clears one that was there;
+// a backward that needs one (label != 0) finds it or records KD_ERR_WORKSPACE, and clears it in
+// both cases, since what was kept is used up.  WS_FOUND_WORD tells kept_dz_kernel.
 constexpr int64_t PREP_ONE_BLOCK = 4096;      // rows
 __global__ void __launch_bounds__(1024)
 prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict__ grad, int64_t T,
                    int64_t V, int32_t* __restrict__ idx_sorted, float* __restrict__ p_sorted,
-                   float2* __restrict__ stats, uint32_t* status) {
-  if (gridDim.x == 1) {
-    // before the next kernel may start: its waits read the word, and a call's word may hold
+                   float2* __restrict__ stats, uint32_t* status, uint64_t label) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    // before the next kernel may start: its waits read the status, and a call's may hold
     // anything (an earlier call's timeout, a fresh allocation's bytes)
-    if (threadIdx.x == 0) {
-      *status = 0u;
-      __threadfence();
+    if (gridDim.x == 1) *status = 0u;
+    uint64_t* at = reinterpret_cast<uint64_t*>(status + WS_LABEL_WORD);
+    if (grad && label) {
+      const bool found = *at == label;
+      status[WS_FOUND_WORD] = found;
+      if (!found) set_status(status, KD_ERR_WORKSPACE);
     }
-    __syncthreads();
+    *at = grad ? 0u : label;
+    __threadfence();
   }
+  if (gridDim.x == 1) __syncthreads();
   griddep_launch_dependents();
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < T;
        t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -361,7 +370,8 @@ __global__ void __launch_bounds__(256)
 kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float zscale, float inv_tau,
                const float* __restrict__ block_max, int64_t ld_max, const float* __restrict__ lse,
                const float* __restrict__ logp, const float* __restrict__ grad_loss,
-               const int32_t* __restrict__ target, const float2* __restrict__ stats) {
+               const int32_t* __restrict__ target, const float2* __restrict__ stats,
+               const uint32_t* __restrict__ status) {
   constexpr int VEC = 16 / sizeof(Elem), COLS = 32 * VEC, BLOCKS = COLS / 32, EACH = KEPT_ROWS / 8;
   __shared__ float scale[KEPT_ROWS][BLOCKS];
   __shared__ int32_t ys[KEPT_ROWS];
@@ -369,7 +379,9 @@ kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float z
   griddep_wait();                       // the prepared rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * KEPT_ROWS;
-  const float coef = (grad_loss ? __ldg(grad_loss) : 1.f) * inv_tau;
+  // without the forward's label, what lies here is something else: NaN, and no wrong gradient
+  const bool found = status[WS_FOUND_WORD] != 0u;
+  const float coef = found ? (grad_loss ? __ldg(grad_loss) : 1.f) * inv_tau : NAN;
   for (int64_t col0 = static_cast<int64_t>(blockIdx.y) * COLS; col0 < V;
        col0 += static_cast<int64_t>(gridDim.y) * COLS) {
     // this lane's vectors, on their way while the factors are formed
@@ -387,7 +399,9 @@ kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float z
       float k = 0.f;
       if (t < T && block * 32 < V) {
         const float S = stats[t].x, m = block_max[block * ld_max + t];
-        if (S != 0.f && m != -INFINITY)
+        if (!found)
+          k = NAN;
+        else if (S != 0.f && m != -INFINITY)
           k = coef * S * ex2_approx(fmaf(m, zscale, -lse[t] * 1.4426950408889634f));
       }
       scale[lane][warp] = k;
@@ -604,14 +618,16 @@ cudaError_t launch_prep(const RowTerms& rt, int64_t T, int64_t V, float inv_tau,
   const int logprob = (rt.flags & KD_KL_LOGPROB_CACHE) ? 1 : 0;
   const bool clears = rt.targets && T <= PREP_ONE_BLOCK;
   if (!clears) {
-    const cudaError_t e = cudaMemsetAsync(status, 0, 4, s);
+    // (the target kernel sees to the label by itself)
+    const cudaError_t e = cudaMemsetAsync(status, 0, rt.targets ? 4 : WS_HEADER_BYTES, s);
     if (e != cudaSuccess) return e;
   }
   if (rt.targets) {
     const int64_t b = clears ? 1 : (T + 1023) / 1024;
     const int64_t threads = T < 1024 ? (T + 31) / 32 * 32 : 1024;
     prep_target_kernel<<<static_cast<unsigned>(b < cap ? b : cap), static_cast<unsigned>(threads),
-                         0, s>>>(rt.targets, rt.grad_rows, T, V, idx_s, p_s, stats, status);
+                         0, s>>>(rt.targets, rt.grad_rows, T, V, idx_s, p_s, stats, status,
+                                 rt.keep_label);
   } else if (rt.K <= PREP_REG_MAXK) {
     const unsigned blocks = static_cast<unsigned>(blocks64 < cap ? blocks64 : cap);
     prep_reg_kernel<<<blocks, PREP_WARPS * 32, 0, s>>>(rt.t_vals, rt.t_idx, T, rt.K, V, inv_tau,
@@ -915,8 +931,8 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
     const dim3 grid(cdiv(T, KEPT_ROWS), cols < 65535 ? cols : 65535);
     if (launch_pdl(kept_dz_kernel<Elem>, grid, 256u, s, dz, L.ldz, T, V, zscale, inv_T_tau,
                    reinterpret_cast<const float*>(w + K.block_max), K.ld_max, lse, rt.kept_logp,
-                   grad_loss, static_cast<const int32_t*>(idx_s),
-                   static_cast<const float2*>(stats)) != cudaSuccess)
+                   grad_loss, static_cast<const int32_t*>(idx_s), static_cast<const float2*>(stats),
+                   static_cast<const uint32_t*>(status)) != cudaSuccess)
       return KD_ERR_CUDA;
   }
   for (int64_t g0 = 0; g0 < T; g0 += group_rows) {

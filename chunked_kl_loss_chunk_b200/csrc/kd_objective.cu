@@ -643,7 +643,10 @@ __global__ void __launch_bounds__(OBJ_THREADS) policy_count_all_kernel(const Pol
                   sm);
   if (threadIdx.x == 0) {
     a.count[blockIdx.x] = n;
-    if (blockIdx.x == 0) *a.status = *a.ticket = 0u;
+    if (blockIdx.x == 0) {
+      clear_status(a.status);
+      *a.ticket = 0u;
+    }
   }
 }
 
@@ -653,7 +656,10 @@ __global__ void __launch_bounds__(OBJ_THREADS) policy_clear_kernel(const PolicyA
                                                                    int32_t counts) {
   griddep_launch_dependents();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * OBJ_THREADS + threadIdx.x;
-  if (i == 0) *a.status = *a.ticket = 0u;
+  if (i == 0) {
+    clear_status(a.status);
+    *a.ticket = 0u;
+  }
   if (i < counts) a.count[i] = 0u;
 }
 
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(OBJ_THREADS, 1) policy_one_kernel(const Policy
   const PolicyQueue queue{rows + warp * PolicyQueue::WARP + 16 * lane};
   PolicyAhead ahead;
   policy_start<OLD, REF>(a, queue, warp, NW, ahead, lane);
-  if (threadIdx.x == 0) *a.status = 0u;
+  if (threadIdx.x == 0) clear_status(a.status);
   uint32_t n_all = 0;
   if (a.mask && a.reduction == KD_REDUCE_SEQUENCE) {
     for (int32_t b = threadIdx.x; b < a.seq.S; b += OBJ_THREADS) a.count[b] = 0u;
@@ -1029,7 +1035,7 @@ __global__ void __launch_bounds__(OBJ_THREADS, PREF_BLOCKS_PER_SM)
 pref_sums_kernel(const PrefArgs a) {
   __shared__ __align__(16) unsigned char rows[OBJ_THREADS / 32 * PREF_SMEM];
   griddep_launch_dependents();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
+  if (blockIdx.x == 0 && threadIdx.x == 0) clear_status(a.status);
   const int warp = threadIdx.x >> 5;
   const int32_t i = blockIdx.x * (OBJ_THREADS / 32) + warp;
   if (i < a.n_spans) pref_sums<SHORT>(a, rows + warp * PREF_SMEM, i, threadIdx.x & 31);
@@ -1073,7 +1079,7 @@ __global__ void __launch_bounds__(OBJ_THREADS, 1) pref_one_kernel(const PrefArgs
   __shared__ double sm[OBJ_THREADS / 32];
   constexpr int NW = OBJ_THREADS / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) *a.status = 0u;
+  if (threadIdx.x == 0) clear_status(a.status);
   for (int32_t i = warp; i < a.n_spans; i += NW)
     pref_sums<SHORT>(a, rows + warp * PREF_SMEM, i, lane);
   __syncthreads();

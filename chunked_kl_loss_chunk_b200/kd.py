@@ -635,7 +635,8 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
     256 positions each).
     ``need=(dH, dW)`` leaves out a gradient that is not wanted (None in its
     place).  ``kept_logp`` and ``ws`` of a forward with ``keep=True``: its
-    exponentials take the place of recomputed logits, and are used up."""
+    exponentials take the place of recomputed logits, and are used up.  A ``ws`` that
+    does not hold them (any more) gives NaN, and KD_ERR_WORKSPACE in it."""
     load()
     if stream is None and _native is not None and dH is None and dW is None and not accumulate_dW and any(need) and \
             (dW_dtype is torch.float32 or dW_dtype is torch.bfloat16):

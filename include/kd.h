@@ -49,7 +49,8 @@ typedef enum kd_status {
   KD_OK = 0,
   KD_ERR_INVALID_ARG = 1,  /* null/misaligned pointer, non-positive size, K > V, bad tau ... */
   KD_ERR_UNSUPPORTED = 2,  /* well-formed but outside the supported ranges          */
-  KD_ERR_WORKSPACE = 3,    /* ws_bytes smaller than the matching *_workspace_size   */
+  KD_ERR_WORKSPACE = 3,    /* ws_bytes smaller than the matching *_workspace_size;  */
+                           /* on the device: ws without what it should hold         */
   KD_ERR_BAD_INDEX = 4,    /* device: a cache index outside [0,V) or repeated in a row */
   KD_ERR_TIMEOUT = 5,      /* device: a pipeline wait exceeded its time limit        */
   KD_ERR_CUDA = 6,         /* a CUDA runtime/driver call failed                      */
@@ -276,7 +277,8 @@ size_t kd_head_logprob_workspace_size(int64_t T, int64_t d, int64_t V, int64_t c
  * keep != 0 (T <= 2 chunk, else KD_ERR_UNSUPPORTED; KD_HEAD_KEEP's workspace)
  * leaves the exponentials of the logits in ws, in the operands' type, for ONE
  * kd_head_logprob_bwd on the same ws, inputs and sizes: it then need not project
- * again.  Nothing else may use ws in between.  A target outside [0, V)
+ * again.  Nothing else may use ws in between: every call that takes ws clears the
+ * label that the backward looks for.  A target outside [0, V)
  * other than KD_TARGET_IGNORE is recorded as KD_ERR_BAD_INDEX, and the logp of its
  * row is NaN; the other rows are as ever.
  */
@@ -295,7 +297,9 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
  *   one is formed: T <= 2 chunk and accumulate_dW == 0 (KD_ERR_UNSUPPORTED
  *   otherwise).
  * kept_logp: the logp of the forward that kept its exponentials in this ws, which
- * this call uses up; NULL: the logits are recomputed.  The kept ones are rounded
+ * this call uses up; NULL: the logits are recomputed.  A ws that does not hold them
+ * (another call has used it since, a second use, other sizes, chunk, temperature or type) is
+ * recorded as KD_ERR_WORKSPACE, and the gradients are NaN.  The kept ones are rounded
  * once more (each dz entry but the target's has two roundings in place of one).
  * A row with a bad target (recorded as KD_ERR_BAD_INDEX) adds nothing to either.
  * Either of dH and dW may be NULL: that gradient is not computed (a frozen head
@@ -428,8 +432,8 @@ kd_status kd_grad_clip(const void* const* grads, void* const* outs, const int64_
                        float* norm, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, then returns the device status recorded in `ws`
- * (KD_OK, KD_ERR_BAD_INDEX, KD_ERR_TIMEOUT or, in the debug build,
- * KD_ERR_INTERNAL), or KD_ERR_CUDA.  Works for the workspaces of every entry
+ * (KD_OK, KD_ERR_BAD_INDEX, KD_ERR_WORKSPACE, KD_ERR_TIMEOUT or, in the debug
+ * build, KD_ERR_INTERNAL), or KD_ERR_CUDA.  Works for the workspaces of every entry
  * point above. */
 kd_status kd_read_device_status(const void* ws, void* stream);
 
