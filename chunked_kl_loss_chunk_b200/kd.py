@@ -691,22 +691,32 @@ def head_logprobs_bwd(h, W, targets, lse, grad_logp, chunk: int, temperature: fl
 
 
 class HeadLogprobs(torch.autograd.Function):
-    """``logp = HeadLogprobs.apply(h, W, targets, chunk, temperature=1.0)``: the
-    log-probabilities of ``head_logprobs`` (NaN for a target that is neither a token
-    nor KD_TARGET_IGNORE) with gradients to h and W (W's in W's dtype).  Up to two chunks of positions the forward keeps what the
-    backward needs of the logits (2 V bytes per position for bf16, in the
-    workspace that the backward needs anyway); beyond, the backward recomputes
-    them chunk by chunk."""
+    """``logp = HeadLogprobs.apply(h, W, targets, chunk, temperature=1.0, keep=None)``:
+    the log-probabilities of ``head_logprobs`` (NaN for a target that is neither a token
+    nor KD_TARGET_IGNORE) with gradients to h and W (W's in W's dtype).
+
+    ``keep=True`` (up to two chunks of positions, of at least 256 each): the forward
+    holds a workspace of kd_head_logprob_workspace_size(..., KD_HEAD_KEEP) bytes until
+    its backward, one for each such forward of a graph, and the backward does not
+    project again.  That is two chunks of exponentials in the operands' type, also where
+    T is one chunk (4 V bytes per position then, for bf16, and 2 V for T of two chunks),
+    V / 8 bytes per position of their references, and 16 d bytes per position of a chunk
+    for the partials of dH: 1.26 GB at T = chunk = 2048, d = 4096, V = 131072.  The kept
+    exponentials are rounded to the operands' type, one rounding more of each dz entry.
+    ``keep=False``: nothing is held, and the backward recomputes the logits chunk by
+    chunk, as it does beyond two chunks.  None keeps where that is possible."""
 
     @classmethod
-    def apply(cls, h, W, targets, chunk, temperature=1.0):
+    def apply(cls, h, W, targets, chunk, temperature=1.0, keep=None):
         if not torch.is_grad_enabled():          # nothing will ask for what a forward keeps
             return head_logprobs(h.detach(), W.detach(), targets, chunk, temperature)[0]
-        return super().apply(h, W, targets, chunk, temperature)
+        return super().apply(h, W, targets, chunk, temperature, keep)
 
     @staticmethod
-    def forward(ctx, h, W, targets, chunk, temperature):
-        keep = any(ctx.needs_input_grad[:2]) and _one_group(h.shape[0], chunk)
+    def forward(ctx, h, W, targets, chunk, temperature, keep):
+        if keep is None:
+            keep = _one_group(h.shape[0], chunk)
+        keep = bool(keep) and any(ctx.needs_input_grad[:2])
         logp, lse, ws = head_logprobs(h, W, targets, chunk, temperature, keep=keep)
         ctx.save_for_backward(h, W, targets, lse, logp if keep else None)
         ctx.chunk, ctx.temperature = chunk, temperature
@@ -725,7 +735,7 @@ class HeadLogprobs(torch.autograd.Function):
                                       need=ctx.needs_input_grad[:2], ws=ws,
                                       kept_logp=None if ws is None else kept,
                                       dW_dtype=W.dtype if direct else torch.float32)
-        return dH, None if dW is None else dW.to(W.dtype), None, None, None
+        return dH, None if dW is None else dW.to(W.dtype), None, None, None, None
 
 
 # ------------------------------------------------- objectives over token log-probabilities

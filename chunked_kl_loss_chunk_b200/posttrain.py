@@ -31,15 +31,16 @@ class Step(NamedTuple):
 
 
 def _through_head(h, W, targets, objective, objective_bytes, cu_seqlens, options, chunk, temperature, ws, dW,
-                  accumulate_dW):
+                  accumulate_dW, keep):
     for name in ("grad", "stream"):        # the step needs the gradient, and all of it on one stream
         if name in options:
             raise TypeError(f"{name}: not an option of a step")
     flat = targets.reshape(-1)
     # up to two chunks the forward keeps what the backward needs of the logits (a given workspace
-    # decides by its size)
-    keep = kd._one_group(h.shape[0], chunk)
-    if keep and ws is not None:
+    # decides by its size), unless the caller has decided
+    decided = keep is not None
+    keep = keep if decided else kd._one_group(h.shape[0], chunk)
+    if keep and not decided and ws is not None:
         keep = ws.numel() >= kd.kd_head_logprob_workspace_size(*h.shape, W.shape[0], chunk, kd._dtype_code(h),
                                                                kd.KD_HEAD_KEEP)
     logp, lse, ws = kd.head_logprobs(h, W, flat, chunk, temperature, ws=ws, backward=True, keep=keep)
@@ -61,7 +62,8 @@ def _through_head(h, W, targets, objective, objective_bytes, cu_seqlens, options
 
 
 def policy_step(h, W, targets, old_logp, advantages, *, chunk: int, temperature: float = 1.0, ref_logp=None,
-                cu_seqlens=None, ws=None, dW=None, accumulate_dW: bool = False, **options) -> Step:
+                cu_seqlens=None, ws=None, dW=None, accumulate_dW: bool = False, keep: bool | None = None,
+                **options) -> Step:
     """Clipped policy loss of sampled answers and its gradients.
 
     h [T, d], W [V, d]; ``targets`` int32 [sequences, tokens], or [T] with
@@ -70,19 +72,23 @@ def policy_step(h, W, targets, old_logp, advantages, *, chunk: int, temperature:
     ``old_logp``, ``ref_logp`` like ``targets``; ``options`` go to
     ``kd.policy_loss`` (clip_low, clip_high, kl_coef, reduction, denom,
     advantages_per).  For micro-batches, ``reduction="fixed"`` with the batch's
-    token count and ``accumulate_dW=True`` add up to the batch's gradient."""
+    token count and ``accumulate_dW=True`` add up to the batch's gradient.
+    ``keep``: whether the forward through the head keeps its exponentials for the
+    backward, as in ``kd.head_logprobs``; None: where T is at most two chunks and a
+    given ``ws`` is large enough."""
     return _through_head(h, W, targets, lambda logp, mask, own: kd.policy_loss(
         logp, old_logp, advantages, mask=mask, ref_logp=ref_logp, cu_seqlens=cu_seqlens, ws=own, **options),
-        kd.kd_policy_loss_workspace_size, cu_seqlens, options, chunk, temperature, ws, dW, accumulate_dW)
+        kd.kd_policy_loss_workspace_size, cu_seqlens, options, chunk, temperature, ws, dW, accumulate_dW, keep)
 
 
 def preference_step(h, W, targets, *, chunk: int, temperature: float = 1.0, ref_logp=None, cu_seqlens=None,
-                    ws=None, dW=None, accumulate_dW: bool = False, **options) -> Step:
+                    ws=None, dW=None, accumulate_dW: bool = False, keep: bool | None = None, **options) -> Step:
     """Paired preference loss of compared answers and its gradients.
 
     ``targets`` as for ``policy_step``, over 2 pairs sequences: the chosen
-    answers, then the rejected ones.  ``options`` go to ``kd.preference_loss``
+    answers, then the rejected ones.  ``keep`` as there.  ``options`` go to ``kd.preference_loss``
     (kind, beta, margin, label_smoothing, length_normalize, pairs_total)."""
     return _through_head(h, W, targets, lambda logp, mask, own: kd.preference_loss(
         logp, ref_logp=ref_logp, mask=mask, cu_seqlens=cu_seqlens, ws=own, **options),
-        lambda n_seqs, n: kd.kd_preference_loss_workspace_size(max(n_seqs // 2, 1), n), cu_seqlens, options, chunk, temperature, ws, dW, accumulate_dW)
+        lambda n_seqs, n: kd.kd_preference_loss_workspace_size(max(n_seqs // 2, 1), n), cu_seqlens, options, chunk,
+        temperature, ws, dW, accumulate_dW, keep)
