@@ -96,12 +96,14 @@ def kd_clip_compute(grads, max_norm, sumsq=None):
 
 def clip_grad_norm(replicated, sharded, max_norm: float, *, compute: Callable = kd_clip_compute,
                    group=None, device=None):
-    """Clips a data-parallel step's gradients in place to the norm over the whole
-    batch, and returns that norm (the same on every rank).
+    """Clips the parameters' gradients of a data-parallel step in place to their norm
+    over the whole batch, and returns that norm (the same on every rank).  (dH is the
+    gradient of an activation; what the trunk makes of it belongs here, dH does not.)
 
     `replicated`: tensors that every rank holds alike (dW after ``shard_step``), counted
     once whichever ranks hold them, but a rank holds all of them or none; `sharded`: each
-    rank's own part of what is split over the ranks, whose sums of squares are added.
+    rank's own part of gradients that are split over the ranks (optimiser shards, rows of
+    an embedding), whose sums of squares are added.
     Either may be empty, also on some ranks only: every rank joins the one all-reduce
     (of three fp64 values on `device`, by default the tensors')."""
     replicated = [t for t in replicated if t.numel()]

@@ -5,8 +5,13 @@ A step is three calls of ``kd``: the log-probabilities of the answers' tokens
 (``head_logprobs``), an objective over them with its gradient for each token
 (``policy_loss`` or ``preference_loss``), and the way of that gradient back into
 h and W (``head_logprobs_bwd``); the [T, V] logits are never materialised, and
-one workspace serves both passes through the head.  ``kd.clip_grad_norm`` (or
-``dp.clip_grad_norm`` over ranks) then clips the step's gradients.
+one workspace serves both passes through the head.  dH goes back into the trunk
+behind the head; ``kd.clip_grad_norm`` (or ``dp.clip_grad_norm`` over ranks) then clips
+dW together with the trunk's parameter gradients.  (dH itself is no parameter's gradient
+and has no part in that norm.)
+
+Positions without a target may hold anything, NaN included, in h as in the arrays of the
+objectives.
 
 Nothing synchronises, so a step can be captured in a CUDA graph.
 """

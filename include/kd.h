@@ -51,7 +51,8 @@ typedef enum kd_status {
   KD_ERR_UNSUPPORTED = 2,  /* well-formed but outside the supported ranges          */
   KD_ERR_WORKSPACE = 3,    /* ws_bytes smaller than the matching *_workspace_size;  */
                            /* on the device: ws without what it should hold         */
-  KD_ERR_BAD_INDEX = 4,    /* device: a cache index outside [0,V) or repeated in a row */
+  KD_ERR_BAD_INDEX = 4,    /* device: a cache index outside [0,V) or repeated in a row,
+                              a target outside [0,V), a cu_seqlens that is none     */
   KD_ERR_TIMEOUT = 5,      /* device: a pipeline wait exceeded its time limit        */
   KD_ERR_CUDA = 6,         /* a CUDA runtime/driver call failed                      */
   KD_ERR_INTERNAL = 7      /* device: an internal invariant failed (checked only in
@@ -398,8 +399,8 @@ kd_status kd_preference_loss(const float* logp, const float* ref_logp, const uin
                              void* stream);
 
 /* ------------------------------------------------------------------------ */
-/* The global norm of a list of gradients (dH, dW and whatever else the step */
-/* has), and clipping to it.  grads, outs, numels and dtypes are HOST arrays */
+/* The global norm of a list of gradients (dW and those of the step's other  */
+/* parameters), and clipping to it.  grads, outs, numels and dtypes are HOST arrays */
 /* of n_tensors >= 1 entries, read during the call (a captured graph keeps   */
 /* the addresses in them).  Tensors are dense, KD_DTYPE_F32 or KD_DTYPE_BF16,*/
 /* may be empty (numels 0), and need only the alignment of their elements:   */
