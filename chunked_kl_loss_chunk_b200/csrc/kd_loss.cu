@@ -265,12 +265,15 @@ prep_reg_kernel(const float* __restrict__ vals, const int32_t* __restrict__ idx,
 //
 // The label of kept exponentials: a forward writes its own, or clears one that was there;
 // a backward that needs one (label != 0) finds it or records KD_ERR_WORKSPACE, and clears it in
-// both cases, since what was kept is used up.  WS_FOUND_WORD tells kept_dz_kernel.
+// both cases, since what was kept is used up.  WS_FOUND_WORD tells kept_dz_kernel.  A
+// forward of the same sizes has the same label, so each row's log-probability `given` is
+// compared with what the forward left in the workspace (`left`): NaN for a row of another.
 constexpr int64_t PREP_ONE_BLOCK = 4096;      // rows
 __global__ void __launch_bounds__(1024)
 prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict__ grad, int64_t T,
                    int64_t V, int32_t* __restrict__ idx_sorted, float* __restrict__ p_sorted,
-                   float2* __restrict__ stats, uint32_t* status, uint64_t label) {
+                   float2* __restrict__ stats, uint32_t* status, uint64_t label,
+                   const float* __restrict__ given, const float* __restrict__ left) {
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     // before the next kernel may start: its waits read the status, and a call's may hold
     // anything (an earlier call's timeout, a fresh allocation's bytes)
@@ -290,7 +293,11 @@ prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict_
        t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int32_t y = targets[t];
     const bool ok = y >= 0 && static_cast<int64_t>(y) < V;
-    const float p = !ok ? 0.f : (grad ? -grad[t] : 1.f);
+    float p = !ok ? 0.f : (grad ? -grad[t] : 1.f);
+    if (given && ok && __float_as_uint(given[t]) != __float_as_uint(left[t])) {
+      p = NAN;
+      set_status(status, KD_ERR_WORKSPACE);
+    }
     idx_sorted[t] = ok ? y : INT32_MAX;
     p_sorted[t] = p;
     const bool bad = !ok && y != KD_TARGET_IGNORE;
@@ -304,7 +311,8 @@ prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict_
 // row; lane l merges tiles l, l+32, ... in order, then a fixed shuffle tree.
 //   LSE_t = M/tau + ln S,  KL_t = sum p log p - G/tau + (sum p) LSE_t
 // or, with LOGP (one target per row, p = 1 at it):
-//   logp_t = G/tau - LSE_t, and the second statistic for a row without a target (p = 0).
+//   logp_t = G/tau - LSE_t, and the second statistic for a row without a target (p = 0);
+// a keeping forward leaves it in the workspace too (`left`, else null).
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void merge_lse(float& m, float& s, float m2, float s2, float zs) {
   const float nm = fmaxf(m, m2);
@@ -317,7 +325,7 @@ template <bool LOGP>
 __global__ void __launch_bounds__(256)
 combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64_t row0,
                float zscale, float inv_tau, const float2* __restrict__ stats,
-               float* __restrict__ lse, float* __restrict__ kl) {
+               float* __restrict__ lse, float* __restrict__ kl, float* __restrict__ left) {
   griddep_launch_dependents();
   griddep_wait();                       // the chunk's GEMM has written the partials
   const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -353,8 +361,13 @@ combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64
     const float L = m * inv_tau + logf(s);
     const float2 st = stats[t];
     lse[t] = L;
-    if constexpr (LOGP) kl[t] = st.x != 0.f ? gsum * inv_tau - L : st.y;
-    else kl[t] = st.y - gsum * inv_tau + st.x * L;
+    if constexpr (LOGP) {
+      const float logp = st.x != 0.f ? gsum * inv_tau - L : st.y;
+      kl[t] = logp;
+      if (left) left[t] = logp;
+    } else {
+      kl[t] = st.y - gsum * inv_tau + st.x * L;
+    }
   }
 }
 
@@ -371,7 +384,7 @@ kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float z
                const float* __restrict__ block_max, int64_t ld_max, const float* __restrict__ lse,
                const float* __restrict__ logp, const float* __restrict__ grad_loss,
                const int32_t* __restrict__ target, const float2* __restrict__ stats,
-               const uint32_t* __restrict__ status) {
+               const uint32_t* status) {
   constexpr int VEC = 16 / sizeof(Elem), COLS = 32 * VEC, BLOCKS = COLS / 32, EACH = KEPT_ROWS / 8;
   __shared__ float scale[KEPT_ROWS][BLOCKS];
   __shared__ int32_t ys[KEPT_ROWS];
@@ -380,7 +393,8 @@ kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float z
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * KEPT_ROWS;
   // without the forward's label, what lies here is something else: NaN, and no wrong gradient
-  const bool found = status[WS_FOUND_WORD] != 0u;
+  // (a volatile load: one of a constant could move above the wait)
+  const bool found = read_status(status + WS_FOUND_WORD) != 0u;
   const float coef = found ? (grad_loss ? __ldg(grad_loss) : 1.f) * inv_tau : NAN;
   for (int64_t col0 = static_cast<int64_t>(blockIdx.y) * COLS; col0 < V;
        col0 += static_cast<int64_t>(gridDim.y) * COLS) {
@@ -611,8 +625,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, unsigned block, cudaSt
 // One target per row: the target kernel.  A cache with K <= 128: the register sort, a grid small enough to be
 // resident at once, so that the first GEMM (launched with programmatic
 // serialization) can start while it runs.  Larger K: the shared-memory sort.
+// left: the log-probabilities of the forward that kept its exponentials, in the workspace.
 cudaError_t launch_prep(const RowTerms& rt, int64_t T, int64_t V, float inv_tau, int32_t* idx_s,
-                        float* p_s, float2* stats, uint32_t* status, cudaStream_t s, int num_sms) {
+                        float* p_s, float2* stats, uint32_t* status, const float* left,
+                        cudaStream_t s, int num_sms) {
   const int64_t blocks64 = (T + PREP_WARPS - 1) / PREP_WARPS;
   const int64_t cap = static_cast<int64_t>(num_sms) * 8;
   const int logprob = (rt.flags & KD_KL_LOGPROB_CACHE) ? 1 : 0;
@@ -627,7 +643,7 @@ cudaError_t launch_prep(const RowTerms& rt, int64_t T, int64_t V, float inv_tau,
     const int64_t threads = T < 1024 ? (T + 31) / 32 * 32 : 1024;
     prep_target_kernel<<<static_cast<unsigned>(b < cap ? b : cap), static_cast<unsigned>(threads),
                          0, s>>>(rt.targets, rt.grad_rows, T, V, idx_s, p_s, stats, status,
-                                 rt.keep_label);
+                                 rt.keep_label, rt.kept_logp, left);
   } else if (rt.K <= PREP_REG_MAXK) {
     const unsigned blocks = static_cast<unsigned>(blocks64 < cap ? blocks64 : cap);
     prep_reg_kernel<<<blocks, PREP_WARPS * 32, 0, s>>>(rt.t_vals, rt.t_idx, T, rt.K, V, inv_tau,
@@ -825,14 +841,15 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   int32_t* idx_s = reinterpret_cast<int32_t*>(w + L.idx_sorted);
   float* p_s = reinterpret_cast<float*>(w + L.p_sorted);
   float2* stats = reinterpret_cast<float2*>(w + L.stats);
-  float* row = row_out ? row_out : reinterpret_cast<float*>(w + L.kl);
+  float* kl = reinterpret_cast<float*>(w + L.kl);
+  float* row = row_out ? row_out : kl;
   const bool keep = rt.keep_chunk > 0;
   KeepLayout K;
   if (keep) K = keep_layout(T, d, V, rt.keep_chunk, chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
   float4* part = reinterpret_cast<float4*>(w + (keep ? K.part : L.scratch));
 
   const float inv_tau = 1.f / tau;
-  if (launch_prep(rt, T, V, inv_tau, idx_s, p_s, stats, status, s, num_sms) != cudaSuccess)
+  if (launch_prep(rt, T, V, inv_tau, idx_s, p_s, stats, status, nullptr, s, num_sms) != cudaSuccess)
     return KD_ERR_CUDA;
   CUtensorMap tW;
   if (!make_map(&tW, W, F32, d, V, d, BK, 128)) return KD_ERR_CUDA;
@@ -879,7 +896,8 @@ static kd_status fwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
     if (launch_pdl(rt.targets ? combine_kernel<true> : combine_kernel<false>,
                    dim3(cblocks), 256u, s, static_cast<const float4*>(part),
                    static_cast<int>(rows), g.n_tiles, c0, zscale, inv_tau,
-                   static_cast<const float2*>(stats), lse, row) != cudaSuccess)
+                   static_cast<const float2*>(stats), lse, row,
+                   keep ? kl : static_cast<float*>(nullptr)) != cudaSuccess)
       return KD_ERR_CUDA;
   }
   if (!loss) return KD_OK;
@@ -907,7 +925,8 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   Elem* dz = reinterpret_cast<Elem*>(w + L.scratch);
 
   const float inv_tau = 1.f / tau;
-  if (launch_prep(rt, T, V, inv_tau, idx_s, p_s, stats, status, s, num_sms) != cudaSuccess)
+  if (launch_prep(rt, T, V, inv_tau, idx_s, p_s, stats, status,
+                  reinterpret_cast<const float*>(w + L.kl), s, num_sms) != cudaSuccess)
     return KD_ERR_CUDA;
   CUtensorMap tW_k, tW_mn;
   if (!make_map(&tW_k, W, F32, d, V, d, BK, 128)) return KD_ERR_CUDA;     // [V, d], K = d
