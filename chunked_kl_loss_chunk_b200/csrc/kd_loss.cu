@@ -941,6 +941,8 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   // dz of KD_DW_GROUP consecutive chunks is kept side by side, so that dW is
   // updated once per group with K = the group's rows (halving dW's
   // read-modify-write traffic); dz and dH are formed chunk by chunk.
+  // (a chunk larger than the batch is the batch: its multiple may pass 64 bits)
+  if (chunk > T) chunk = T;
   const int64_t group_rows = chunk * KD_DW_GROUP;
   const bool kept = rt.kept_logp != nullptr;   // then one group holds all rows
   if (kept) {
