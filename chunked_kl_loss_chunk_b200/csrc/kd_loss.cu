@@ -328,10 +328,11 @@ combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64
                float* __restrict__ lse, float* __restrict__ kl, float* __restrict__ left) {
   griddep_launch_dependents();
   griddep_wait();                       // the chunk's GEMM has written the partials
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  // (more than 2^32 threads from 2^27 rows on)
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (warp >= rows) return;
-  const float4* pr = partials + static_cast<int64_t>(warp) * n_tiles;
+  const float4* pr = partials + warp * n_tiles;
   float m = -INFINITY, s = 0.f, gsum = 0.f;
   for (int j = lane; j < n_tiles; j += 32) {
     const float4 q = pr[j];
