@@ -10,9 +10,9 @@
 namespace kd {
 
 // Header of every workspace, in 32-bit words: the status at 0, a counter or ticket at 2,
-// the label of what a keeping forward of the head left (64 bits) and whether the backward
-// found the label that it needs.
-constexpr int WS_LABEL_WORD = 4, WS_FOUND_WORD = 6, WS_HEADER_BYTES = 32;
+// the label of what a keeping forward of the head left (64 bits), whether the backward
+// found the label that it needs, and the status before its own.
+constexpr int WS_LABEL_WORD = 4, WS_FOUND_WORD = 6, WS_BEFORE_WORD = 7, WS_HEADER_BYTES = 32;
 
 // Largest number of K-splits used for dH = dz W (its fp32 partials live in
 // the workspace).

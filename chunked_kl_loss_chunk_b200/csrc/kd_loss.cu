@@ -257,15 +257,15 @@ prep_reg_kernel(const float* __restrict__ vals, const int32_t* __restrict__ idx,
 // the gather is z_y.  Backward: p = S = -g_t, so that the dz epilogue's
 //   coef (S softmax - p [v == y])  is  g_t / tau ([v == y] - softmax),
 // the gradient of g_t logp_t.  A row whose target is KD_TARGET_IGNORE gets
-// p = S = 0 and an index past V (its g_t is not read); any other target outside
+// p = S = 0 and an index past V (its g_t is not used); any other target outside
 // [0, V) gets the same and records KD_ERR_BAD_INDEX.  The second statistic is the
 // log-probability of a row without an entry: 0, or NaN for a bad target, so that it
 // does not go unnoticed where nobody reads the status.  A single block also clears
 // the status word, in the place of a memset before it (2 us of a short call).
 //
 // The label of kept exponentials: a forward writes its own, or clears one that was there;
-// a backward that needs one (label != 0) finds it or records KD_ERR_WORKSPACE, and clears it in
-// both cases, since what was kept is used up.  WS_FOUND_WORD tells kept_dz_kernel.  A
+// a backward that needs one (label != 0) finds it, of a forward that was not stopped, or
+// records KD_ERR_WORKSPACE, and clears it in both cases, since what was kept is used up.  WS_FOUND_WORD tells kept_dz_kernel.  A
 // forward of the same sizes has the same label, so each row's log-probability `given` is
 // compared with what the forward left in the workspace (`left`): NaN for a row of another.
 constexpr int64_t PREP_ONE_BLOCK = 4096;      // rows
@@ -274,27 +274,47 @@ prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict_
                    int64_t V, int32_t* __restrict__ idx_sorted, float* __restrict__ p_sorted,
                    float2* __restrict__ stats, uint32_t* status, uint64_t label,
                    const float* __restrict__ given, const float* __restrict__ left) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
+  // the first row's loads are under way while the header is seen to
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  int32_t y = 0;
+  float g = -1.f, here = 0.f, there = 0.f;
+  auto load = [&] {
+    if (t >= T) return;
+    y = targets[t];
+    if (grad) g = grad[t];
+    if (given) {
+      here = given[t];
+      there = left[t];
+    }
+  };
+  load();
+  uint32_t before = 0u;                 // what the forward recorded
+  if (grad && label && threadIdx.x == 0)
+    before = status[gridDim.x == 1 ? 0 : WS_BEFORE_WORD];
+  if (gridDim.x == 1) {
     // before the next kernel may start: its waits read the status, and a call's may hold
     // anything (an earlier call's timeout, a fresh allocation's bytes)
-    if (gridDim.x == 1) *status = 0u;
+    if (threadIdx.x == 0) {
+      *status = 0u;
+      __threadfence();
+    }
+    __syncthreads();
+  }
+  griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     uint64_t* at = reinterpret_cast<uint64_t*>(status + WS_LABEL_WORD);
     if (grad && label) {
-      const bool found = *at == label;
+      const bool found = *at == label && !stops(before);
       status[WS_FOUND_WORD] = found;
       if (!found) set_status(status, KD_ERR_WORKSPACE);
     }
     *at = grad ? 0u : label;
-    __threadfence();
   }
-  if (gridDim.x == 1) __syncthreads();
-  griddep_launch_dependents();
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < T;
-       t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int32_t y = targets[t];
+  for (; t < T; t += step, load()) {
     const bool ok = y >= 0 && static_cast<int64_t>(y) < V;
-    float p = !ok ? 0.f : (grad ? -grad[t] : 1.f);
-    if (given && ok && __float_as_uint(given[t]) != __float_as_uint(left[t])) {
+    float p = ok ? -g : 0.f;
+    if (ok && __float_as_uint(here) != __float_as_uint(there)) {
       p = NAN;
       set_status(status, KD_ERR_WORKSPACE);
     }
@@ -636,7 +656,10 @@ cudaError_t launch_prep(const RowTerms& rt, int64_t T, int64_t V, float inv_tau,
   const bool clears = rt.targets && T <= PREP_ONE_BLOCK;
   if (!clears) {
     // (the target kernel sees to the label by itself)
-    const cudaError_t e = cudaMemsetAsync(status, 0, rt.targets ? 4 : WS_HEADER_BYTES, s);
+    cudaError_t e = cudaSuccess;
+    if (rt.kept_logp)
+      e = cudaMemcpyAsync(status + WS_BEFORE_WORD, status, 4, cudaMemcpyDeviceToDevice, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, rt.targets ? 4 : WS_HEADER_BYTES, s);
     if (e != cudaSuccess) return e;
   }
   if (rt.targets) {

@@ -50,7 +50,8 @@ def _through_head(h, W, targets, objective, objective_bytes, cu_seqlens, options
                                                                kd.KD_HEAD_KEEP)
     logp, lse, ws = kd.head_logprobs(h, W, flat, chunk, temperature, ws=ws, backward=True, keep=keep)
     status = ws[:4].view(torch.int32)
-    found = [status.clone()]           # the backward clears the forward's
+    # the backward clears the forward's; one that uses what a forward kept has seen it
+    found = [] if keep else [status.clone()]
     shaped = logp.view(targets.shape)
     # only packed sequences can be wrong in the objective's device data
     own = None

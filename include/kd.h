@@ -300,7 +300,7 @@ kd_status kd_head_logprob_fwd(const void* h, const void* W, int dtype, int64_t T
  * kept_logp: the logp of the forward that kept its exponentials in this ws, which
  * this call uses up; NULL: the logits are recomputed.  A ws that does not hold them
  * (another call has used it since, another keeping forward also; a second use; other
- * sizes, chunk, temperature or type) is recorded as KD_ERR_WORKSPACE, and the gradients
+ * sizes, chunk, temperature or type; a forward that was stopped) is recorded as KD_ERR_WORKSPACE, and the gradients
  * are NaN.  The kept ones are rounded once more (each dz entry but the target's has two roundings in place of one).
  * A row with a bad target (recorded as KD_ERR_BAD_INDEX) adds nothing to either.
  * Either of dH and dW may be NULL: that gradient is not computed (a frozen head

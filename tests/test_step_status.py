@@ -44,6 +44,7 @@ def test_every_stage_is_heard(monkeypatch, packed, kind, first, objective, secon
     targets, kw = torch.zeros((2, 4), dtype=torch.int32), dict(chunk=4)
     if packed:
         targets, kw["cu_seqlens"] = targets.view(-1), torch.tensor([0, 4, 8], dtype=torch.int32)
+    kw["keep"] = False
     if kind == "policy":
         step = posttrain.policy_step(h, W, targets, torch.zeros(targets.shape), torch.zeros(2), **kw)
     else:
