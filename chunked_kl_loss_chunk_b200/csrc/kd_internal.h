@@ -48,7 +48,7 @@ WsLayout ws_layout(int64_t T, int64_t d, int64_t V, int K, int64_t chunk, int dt
 
 // Workspace of a head log-probability forward that keeps its exponentials for the
 // backward: ws_layout(T, d, V, 1, chunk), whose dz they lie in, then the forward's
-// partials (of fwd_chunk rows) and the reference of each block of 32 exponentials.
+// partials (of fwd_chunk rows; in the backward the copy of h for dW) and the reference of each block of 32 exponentials.
 struct KeepLayout {
   size_t part = 0, block_max = 0, total = 0;
   int64_t ld_max = 0;

@@ -398,6 +398,8 @@ combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64
 // digits where p is near 1) but from logp: coef p (e^logp - 1), p = S = -g.
 // Elementwise over T x V: a pass of the memory (0.18 ms at 2048 x 131072, 6.0 TB/s) in the
 // place of a product (1.6 ms).  A block takes 32 rows x 32 vectors of 16 bytes.
+// h_out (or null): the copy of h that target_rows_kernel makes otherwise, h_vecs vectors a
+// row, which the blocks of these 32 rows share.
 constexpr int KEPT_ROWS = 32;
 template <typename Elem>
 __global__ void __launch_bounds__(256)
@@ -405,7 +407,8 @@ kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float z
                const float* __restrict__ block_max, int64_t ld_max, const float* __restrict__ lse,
                const float* __restrict__ logp, const float* __restrict__ grad_loss,
                const int32_t* __restrict__ target, const float2* __restrict__ stats,
-               const uint32_t* status) {
+               const uint32_t* status, const uint4* __restrict__ h, int64_t h_vecs,
+               uint4* __restrict__ h_out) {
   constexpr int VEC = 16 / sizeof(Elem), COLS = 32 * VEC, BLOCKS = COLS / 32, EACH = KEPT_ROWS / 8;
   __shared__ float scale[KEPT_ROWS][BLOCKS];
   __shared__ int32_t ys[KEPT_ROWS];
@@ -481,23 +484,55 @@ kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float z
     }
     __syncthreads();
   }
+  if (h_out) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.y) * 32 + lane; i < h_vecs;
+         i += static_cast<int64_t>(gridDim.y) * 32) {
+      uint4 v[EACH];
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        const int64_t t = row0 + warp * EACH + k;
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < T && target[t] != INT32_MAX) v[k] = h[t * h_vecs + i];
+      }
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        const int64_t t = row0 + warp * EACH + k;
+        if (t < T) h_out[t * h_vecs + i] = v[k];
+      }
+    }
+  }
 }
 
 // h for dW = dz^T h, with zeros in the rows that have no target: what a trunk left
 // there (NaN of attention over nothing, infinities) times their dz of 0 would be NaN.
-// Elementwise, 16 bytes a thread; the dW GEMM then reads `out` in the place of h.  The
-// copy is made whether or not a row is ignored, which only the device knows: 4 bytes an
-// element beside 6 V flops of each.
+// Elementwise; the dW GEMM then reads `out` in the place of h.  The copy is made whether
+// or not a row is ignored, which only the device knows: 4 bytes an element beside 6 V flops
+// of each, and 4 us of a short call, so that where the exponentials were kept
+// kept_dz_kernel makes it on the way.  A warp takes a row, four 16-byte vectors a lane at a
+// time.
+constexpr int TARGET_ROWS_BLOCKS = 2;   // of an SM
 __global__ void __launch_bounds__(256)
 target_rows_kernel(const uint4* __restrict__ h, const int32_t* __restrict__ target, int64_t rows,
                    int64_t per_row, uint4* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();                       // the prepared rows, and what `out` held before
-  const int64_t n = rows * per_row;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const bool none = target[i / per_row] == INT32_MAX;
-    out[i] = none ? make_uint4(0u, 0u, 0u, 0u) : h[i];
+  const int lane = threadIdx.x & 31;
+  const int64_t step = 128, pieces = (per_row + step - 1) / step;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
+    const bool none = target[r] == INT32_MAX;
+    for (int64_t piece = 0; piece < pieces; ++piece) {
+      const int64_t at = r * per_row + piece * step, end = (r + 1) * per_row;
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (!none && at + 32 * k + lane < end) v[k] = h[at + 32 * k + lane];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (at + 32 * k + lane < end) out[at + 32 * k + lane] = v[k];
+    }
   }
 }
 
@@ -840,8 +875,11 @@ KeepLayout keep_layout(int64_t T, int64_t d, int64_t V, int64_t chunk, int64_t f
   c.ok = L.ok;
   const size_t rows = static_cast<size_t>(fwd_chunk < T ? fwd_chunk : T);
   size_t off = L.total;
+  const size_t part = c.mul(c.mul(rows, static_cast<size_t>((V + BN - 1) / BN)), 16);
+  const size_t h_copy = c.mul(c.mul(static_cast<size_t>(T), static_cast<size_t>(d)),
+                              dtype == KD_DTYPE_F32 ? 4 : 2);
   K.part = off;
-  off = c.align(c.add(off, c.mul(c.mul(rows, static_cast<size_t>((V + BN - 1) / BN)), 16)));
+  off = c.align(c.add(off, part > h_copy ? part : h_copy));
   K.ld_max = (T + 31) / 32 * 32;
   K.block_max = off;
   off = c.align(c.add(off, c.mul(c.mul(static_cast<size_t>((V + 31) / 32),
@@ -969,15 +1007,19 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
   if (chunk > T) chunk = T;
   const int64_t group_rows = chunk * KD_DW_GROUP;
   const bool kept = rt.kept_logp != nullptr;   // then one group holds all rows
+  uint4* h_clean = nullptr;                    // h without what rows hold that have no target
   if (kept) {
     const KeepLayout K =
         keep_layout(T, d, V, chunk, rt.keep_chunk, F32 ? KD_DTYPE_F32 : KD_DTYPE_BF16);
+    // (the forward's partials are done with)
+    if (dW) h_clean = reinterpret_cast<uint4*>(w + K.part);
     const int cols = cdiv(V, 32 * (16 / sizeof(Elem)));
     const dim3 grid(cdiv(T, KEPT_ROWS), cols < 65535 ? cols : 65535);
     if (launch_pdl(kept_dz_kernel<Elem>, grid, 256u, s, dz, L.ldz, T, V, zscale, inv_T_tau,
                    reinterpret_cast<const float*>(w + K.block_max), K.ld_max, lse, rt.kept_logp,
                    grad_loss, static_cast<const int32_t*>(idx_s), static_cast<const float2*>(stats),
-                   static_cast<const uint32_t*>(status)) != cudaSuccess)
+                   static_cast<const uint32_t*>(status), static_cast<const uint4*>(h),
+                   static_cast<int64_t>(d * sizeof(Elem) / 16), h_clean) != cudaSuccess)
       return KD_ERR_CUDA;
   }
   for (int64_t g0 = 0; g0 < T; g0 += group_rows) {
@@ -1061,13 +1103,16 @@ static kd_status bwd_impl(const void* h, const void* W, int64_t T, int64_t T_nor
     // (3) dW (+)= dz_g^T h_g over the group: M = V, N = d, K = grows; both
     //     operands MN-major
     const Elem* hg = static_cast<const Elem*>(h) + g0 * d;
-    if (rt.targets) {
+    if (h_clean) {
+      hg = reinterpret_cast<const Elem*>(h_clean);
+    } else if (rt.targets) {
       // into the place of the dH partials, which the group has done with: at most
       // KD_DW_GROUP rows_pad d operands in KD_DH_MAX_SPLIT rows_pad d floats
       static_assert(KD_DW_GROUP * sizeof(Elem) <= KD_DH_MAX_SPLIT * sizeof(float), "h fits");
       const int64_t per_row = d * sizeof(Elem) / 16;
-      int64_t blocks = (grows * per_row + 255) / 256;
-      if (blocks > 8 * static_cast<int64_t>(num_sms)) blocks = 8 * static_cast<int64_t>(num_sms);
+      int64_t blocks = (grows + 7) / 8;
+      const int64_t most = TARGET_ROWS_BLOCKS * static_cast<int64_t>(num_sms);
+      if (blocks > most) blocks = most;
       if (launch_pdl(target_rows_kernel, dim3(static_cast<unsigned>(blocks)), 256u, s,
                      reinterpret_cast<const uint4*>(hg), static_cast<const int32_t*>(idx_s + g0),
                      grows, per_row, reinterpret_cast<uint4*>(hpart)) != cudaSuccess)
