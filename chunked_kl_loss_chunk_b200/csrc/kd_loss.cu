@@ -402,7 +402,7 @@ combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64
 // row, which the blocks of these 32 rows share.
 constexpr int KEPT_ROWS = 32;
 template <typename Elem>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)      // 64 registers (73 left three blocks an SM: +20%)
 kept_dz_kernel(Elem* __restrict__ dz, int64_t ldz, int64_t T, int64_t V, float zscale, float inv_tau,
                const float* __restrict__ block_max, int64_t ld_max, const float* __restrict__ lse,
                const float* __restrict__ logp, const float* __restrict__ grad_loss,
