@@ -265,9 +265,10 @@ prep_reg_kernel(const float* __restrict__ vals, const int32_t* __restrict__ idx,
 //
 // The label of kept exponentials: a forward writes its own, or clears one that was there;
 // a backward that needs one (label != 0) finds it, of a forward that was not stopped, or
-// records KD_ERR_WORKSPACE, and clears it in both cases, since what was kept is used up.  WS_FOUND_WORD tells kept_dz_kernel.  A
-// forward of the same sizes has the same label, so each row's log-probability `given` is
-// compared with what the forward left in the workspace (`left`): NaN for a row of another.
+// records KD_ERR_WORKSPACE, and clears it in both cases, since what was kept is used up.
+// WS_FOUND_WORD tells kept_dz_kernel.  A forward of the same sizes has the same label, so
+// each row's log-probability `given` is compared with what the forward left in the
+// workspace (`left`): NaN for a row of another.
 constexpr int64_t PREP_ONE_BLOCK = 4096;      // rows
 __global__ void __launch_bounds__(1024)
 prep_target_kernel(const int32_t* __restrict__ targets, const float* __restrict__ grad, int64_t T,
@@ -396,8 +397,8 @@ combine_kernel(const float4* __restrict__ partials, int rows, int n_tiles, int64
 // reference m, coef S exp(a - LSE) = (coef S 2^(m zscale - LSE log2 e)) kept.  The
 // target's entry does not come from the rounded exponential (1 - p would lose its
 // digits where p is near 1) but from logp: coef p (e^logp - 1), p = S = -g.
-// Elementwise over T x V: a pass of the memory (0.18 ms at 2048 x 131072, 6.0 TB/s) in the
-// place of a product (1.6 ms).  A block takes 32 rows x 32 vectors of 16 bytes.
+// Elementwise over T x V: a pass of the memory (0.19 ms at 2048 x 131072, 5.9 TB/s) in the
+// place of a product (1.5 ms).  A block takes 32 rows x 32 vectors of 16 bytes.
 // h_out (or null): the copy of h that target_rows_kernel makes otherwise, h_vecs vectors a
 // row, which the blocks of these 32 rows share.
 constexpr int KEPT_ROWS = 32;

@@ -669,8 +669,8 @@ __global__ void __launch_bounds__(OBJ_THREADS) policy_count_each_kernel(const Po
                     (gridDim.x * blockDim.x) >> 5, threadIdx.x & 31);
 }
 
-// 8.4M tokens, a third of them counting, advantages per token and a reference: 28 us,
-// 5.9 TB/s of what a call has to read and write at most, and 201 instructions a row
+// 8.4M tokens, a third of them counting, advantages per token and a reference: 27 us,
+// 6.1 TB/s of what a call has to read and write at most, and 197 instructions a row
 // (0.6 of the issue slots).  0.8M packed tokens: 15 us, of which most is latency: the
 // first loads, the look-ups, and the reduction over the blocks at the end.
 template <bool OLD, bool REF>

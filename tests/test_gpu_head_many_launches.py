@@ -75,3 +75,26 @@ def test_policy_step(chunk, roundings):
     assert (step.logp.view(-1).double() - rl).abs().max() <= 2e-3
     assert bool(((step.dH.double() - rH).abs() <= (1 + roundings) * EPS * aH + 2e-3 * pH + 1e-30).all())
     assert bool(((step.dW.double() - rW).abs() <= roundings * EPS * aW + 2e-3 * pW + 1e-30).all())
+
+
+def test_captured_and_replayed():
+    """Several launches, the targets in several blocks, kept in one workspace, in a graph."""
+    require_gpu()
+    T, d, V, chunk = 5000, 64, 700, 2500
+    h, W, tgt, g = _inputs(T, d, V, torch.bfloat16, seed=64)
+    ws = kd.alloc_workspace(kd.kd_head_logprob_workspace_size(T, d, V, chunk, kd.KD_DTYPE_BF16, kd.KD_HEAD_KEEP), "cuda")
+
+    def run():
+        logp, lse, _ = kd.head_logprobs(h, W, tgt, chunk, keep=True, ws=ws)
+        return (logp, *kd.head_logprobs_bwd(h, W, tgt, lse, g, chunk, ws=ws, kept_logp=logp)[:2])
+
+    want = [x.clone() for x in run()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for _ in range(3):
+        for x in out:
+            x.zero_()
+        graph.replay()
+        assert kd.read_device_status(ws) == kd.KD_OK
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
